@@ -1,4 +1,5 @@
 """Build libsscan.so (the CUDA library behind include/sscan.h) in-tree for sm_100a."""
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -34,14 +35,29 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         newest = max(os.path.getmtime(p) for p in deps())
         if os.path.getmtime(out) >= newest:
             return out
-    cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", out + ".tmp"] + sources()
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+             "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+             "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     if debug:
-        cmd[1:1] = ["-DSSCAN_DEBUG_BOUNDS=1", "-rdc=true"]
+        flags += ["-DSSCAN_DEBUG_BOUNDS=1", "-rdc=true"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+        flags.append("-Xptxas=-v")
+    # one object per source, compiled side by side; an object newer than its source and
+    # every header is kept
+    objdir = os.path.join(HERE, "_build", "debug" if debug else "release")
+    os.makedirs(objdir, exist_ok=True)
+    headers = max(os.path.getmtime(p) for p in deps() if not p.endswith(".cu"))
+
+    def compile_one(src):
+        obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
+        if force or not os.path.exists(obj) or os.path.getmtime(obj) <= max(headers, os.path.getmtime(src)):
+            subprocess.run([NVCC, *flags, "-c", src, "-o", obj + ".tmp"], check=True)
+            os.replace(obj + ".tmp", obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objects = list(pool.map(compile_one, sources()))
+    subprocess.run([NVCC, *flags[:2], "-shared", *(["-rdc=true"] if debug else []), "-o", out + ".tmp", *objects], check=True)
     os.replace(out + ".tmp", out)
     return out
 
