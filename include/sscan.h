@@ -251,12 +251,110 @@ SSCAN_API sscan_status sscan_bwd_complex(const sscan_problem* problem, const voi
 /* Static, human-readable name of a status code. */
 SSCAN_API const char* sscan_status_string(sscan_status status);
 
+/* ---------------------------------------------------------------------------------
+ * Layers around the scan.  The conventions above hold for all of them: dense row-major
+ * device tensors of the caller, fp32 or bf16 (batch, L, ...) tensors and fp32
+ * parameters, states and parameter gradients, fp32 arithmetic, bf16 results rounded
+ * once, host-side checks before anything is enqueued, `stream` as given, no allocation
+ * and no synchronisation.  Sums over tokens are taken in a fixed order, so two calls on
+ * the same inputs give the same bits.  At most 2^37 elements per (batch, L, ...) tensor.
+ * Two calls that may overlap on the GPU must not share a workspace.
+ * --------------------------------------------------------------------------------- */
+
+/*
+ * Causal depthwise convolution of the block's input branch, per channel d:
+ *   y_t   = bias_d + sum_{k=0}^{K-1} weight_dk x_{t-K+1+k},   K = taps
+ *   out_t = SiLU(y_t) with SSCAN_CONV_SILU, else y_t
+ * x_t = u_t for t >= 0; the K-1 inputs before the sequence come from state0
+ * (batch, K-1, D) in io_dtype, oldest first (NULL = zeros).
+ */
+#define SSCAN_CONV_SILU 1u
+
+typedef struct sscan_conv_problem {
+    int64_t batch;    /* >= 0 */
+    int64_t seqlen;   /* L >= 0 */
+    int64_t dim;      /* D >= 0, channels */
+    int64_t taps;     /* K, 2..4 */
+    int32_t io_dtype; /* sscan_dtype of u, out, the states and their gradients */
+    uint32_t flags;   /* SSCAN_CONV_SILU or 0 */
+} sscan_conv_problem;
+
+/* Bytes of workspace for op SSCAN_OP_BWD (partial sums of the parameter gradients); 0 for
+ * every other op and for an invalid problem. */
+SSCAN_API size_t sscan_conv_workspace_size(const sscan_conv_problem* problem, int op);
+
+/* weight (D, K) fp32; bias (D) fp32 or NULL; state_last (batch, K-1, D), or NULL, receives
+ * the last K-1 inputs (state0's where the sequence is shorter). */
+SSCAN_API sscan_status sscan_conv_fwd(const sscan_conv_problem* problem, const void* u, const float* weight,
+                                      const float* bias, const void* state0, void* out, void* state_last,
+                                      void* stream);
+
+/* Gradients of sum(out * dout): du (batch, L, D) and dstate0 (batch, K-1, D) in io_dtype,
+ * dweight (D, K) and dbias (D) fp32.  dbias and dstate0 may be NULL; dbias only with bias,
+ * dstate0 only with state0.  The pre-activation is recomputed.  batch <= 65535. */
+SSCAN_API sscan_status sscan_conv_bwd(const sscan_conv_problem* problem, const void* u, const float* weight,
+                                      const float* bias, const void* state0, const void* dout, void* du,
+                                      float* dweight, float* dbias, void* dstate0, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* One token: problem->seqlen must be 1; u, out (batch, D); state (batch, K-1, D) in io_dtype
+ * is read and shifted in place.  Equals sscan_conv_fwd with seqlen 1. */
+SSCAN_API sscan_status sscan_conv_step(const sscan_conv_problem* problem, const void* u, const float* weight,
+                                       const float* bias, void* state, void* out, void* stream);
+
+/*
+ * Gated linear recurrence with one state per channel d, both gates per token and channel:
+ *   r_t = sigmoid(a_raw_t + a_bias_d),  i_t = sigmoid(i_raw_t + i_bias_d)
+ *   a_t = exp(-rate softplus(Lam_d) r_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t u_t,   out_t = h_t,   h_{-1} = h0 (zero when NULL)
+ * u, a_raw, i_raw, out (batch, L, D) in io_dtype; Lam, a_bias, i_bias (D) and h0, h_last
+ * (batch, D) fp32; a_bias, i_bias, h0, h_last may be NULL.
+ */
+typedef struct sscan_gated_problem {
+    int64_t batch;    /* >= 0 */
+    int64_t seqlen;   /* L >= 0 */
+    int64_t dim;      /* D >= 0, channels */
+    int32_t io_dtype; /* sscan_dtype of the (batch, L, D) tensors */
+    float rate;       /* > 0, at most 1e6 */
+} sscan_gated_problem;
+
+/* Bytes of workspace for op SSCAN_OP_FWD or SSCAN_OP_BWD (0 when none). */
+SSCAN_API size_t sscan_gated_workspace_size(const sscan_gated_problem* problem, int op);
+
+/* Rows per sequence of the checkpoints that sscan_gated_fwd can save for the backward. */
+SSCAN_API int64_t sscan_gated_checkpoints(const sscan_gated_problem* problem);
+
+/* checkpoints: NULL, or (batch, sscan_gated_checkpoints(problem), D) fp32, which receives the
+ * state before every 64th step.  The sequence is split over the GPU in one pass: each tile
+ * waits, boundedly, for the carry of tiles that started before it. */
+SSCAN_API sscan_status sscan_gated_fwd(const sscan_gated_problem* problem, const void* u, const void* a_raw,
+                                       const void* i_raw, const float* Lam, const float* a_bias,
+                                       const float* i_bias, const float* h0, void* out, float* h_last,
+                                       float* checkpoints, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out * dout).  checkpoints: those of a forward call on the same inputs, or
+ * NULL (recomputed by a pass of their own).  du, da_raw, di_raw in io_dtype; dLam, da_bias,
+ * di_bias (D) and dh0 (batch, D) fp32; da_bias, di_bias and dh0 may be NULL, the first two
+ * only given with their bias.  Where rate softplus(Lam) r underflows to zero, sqrt(1 - a^2)
+ * has no finite slope and that term of da_raw and dLam is taken as zero. */
+SSCAN_API sscan_status sscan_gated_bwd(const sscan_gated_problem* problem, const void* u, const void* a_raw,
+                                       const void* i_raw, const float* Lam, const float* a_bias,
+                                       const float* i_bias, const float* h0, const float* checkpoints,
+                                       const void* dout, void* du, void* da_raw, void* di_raw, float* dLam,
+                                       float* da_bias, float* di_bias, float* dh0, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* One token: problem->seqlen must be 1; u, a_raw, i_raw, out (batch, D); state (batch, D) fp32
+ * is read and overwritten in place. */
+SSCAN_API sscan_status sscan_gated_step(const sscan_gated_problem* problem, const void* u, const void* a_raw,
+                                        const void* i_raw, const float* Lam, const float* a_bias,
+                                        const float* i_bias, float* state, void* out, void* stream);
+
 /* One-line reason for the most recent failed call on this thread ("" if none). */
 SSCAN_API const char* sscan_last_error(void);
 
-/* Number of kernels the most recent sscan_fwd / sscan_fwd_noalloc /
- * sscan_last_state / sscan_bwd call on this thread enqueued (memsets and copies
- * not counted). */
+/* Number of kernels the most recent compute call on this thread enqueued (memsets and
+ * copies not counted). */
 SSCAN_API int sscan_last_launch_count(void);
 
 /* 1 in the debug build of the library (libsscan_debug.so), whose kernels check every
@@ -269,8 +367,8 @@ SSCAN_API int sscan_debug_bounds(void);
  * Device-side status of the library's kernels on the current device: *flags
  * receives the OR of every error bit raised since the last clear (bit 0: in a
  * forward kernel, bit 1: in the backward kernel, a bounded wait for an
- * asynchronous tile copy gave up, so that kernel stopped early and its outputs
- * are incomplete; bit 2: sscan_probe_wait_timeout's wait ran out, as it is meant
+ * asynchronous tile copy, or for an earlier tile's carry, gave up, so that the
+ * kernel's outputs are incomplete or wrong; bit 2: sscan_probe_wait_timeout's wait ran out, as it is meant
  * to; bit 3, debug build only: an index out of its array's range was caught and the
  * access skipped).  Returns SSCAN_ERR_TIMEOUT when any bit is set, SSCAN_OK when none is.
  * clear != 0 resets the word after reading.  Synchronous: it waits for work

@@ -40,6 +40,16 @@ class Problem(ctypes.Structure):
                 ("dstate", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class ConvProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("taps", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class GatedProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("rate", ctypes.c_float)]
+
+
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libsscan.so (built in-tree by ``selective_state_space_33_b200/build.py``)."""
     global _lib
@@ -69,6 +79,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sscan_carry.restype = ctypes.c_int
     lib.sscan_step.argtypes = [pp] + [vp] * 10 + [vp]
     lib.sscan_step.restype = ctypes.c_int
+    cp, gp = ctypes.POINTER(ConvProblem), ctypes.POINTER(GatedProblem)
+    lib.sscan_conv_workspace_size.argtypes = [cp, ctypes.c_int]
+    lib.sscan_conv_workspace_size.restype = sz
+    lib.sscan_conv_fwd.argtypes = [cp] + [vp] * 6 + [vp]
+    lib.sscan_conv_bwd.argtypes = [cp] + [vp] * 10 + [sz, vp]
+    lib.sscan_conv_step.argtypes = [cp] + [vp] * 5 + [vp]
+    lib.sscan_gated_workspace_size.argtypes = [gp, ctypes.c_int]
+    lib.sscan_gated_workspace_size.restype = sz
+    lib.sscan_gated_checkpoints.argtypes = [gp]
+    lib.sscan_gated_checkpoints.restype = ctypes.c_int64
+    lib.sscan_gated_fwd.argtypes = [gp] + [vp] * 11 + [sz, vp]
+    lib.sscan_gated_bwd.argtypes = [gp] + [vp] * 17 + [sz, vp]
+    lib.sscan_gated_step.argtypes = [gp] + [vp] * 8 + [vp]
+    for f in ("conv_fwd", "conv_bwd", "conv_step", "gated_fwd", "gated_bwd", "gated_step"):
+        getattr(lib, "sscan_" + f).restype = ctypes.c_int
     lib.sscan_status_string.argtypes = [ctypes.c_int]
     lib.sscan_status_string.restype = ctypes.c_char_p
     lib.sscan_last_error.argtypes = []
@@ -362,6 +387,212 @@ def sscan_carry(P, H, h0=None, *, stream=None):
     _check(load_library().sscan_carry(ctypes.byref(prob), int(K), _ptr(P), _ptr(H), _ptr(h0), _ptr(carry),
                                       _ptr(h_final), _stream(stream)))
     return carry, h_final
+
+
+# ---------------------------------------------------------------- layers around the scan
+
+SSCAN_CONV_SILU = 1
+
+
+def _at(t):
+    """Device address as an integer (None for no tensor), which ctypes takes for a void*."""
+    return None if t is None else t.data_ptr()
+
+
+def _on(device, stream, body):
+    """body(raw stream) with `device` current and allocations made for the stream that the
+    kernels run on, so that a workspace freed on return is not reused before they are done."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(torch.cuda.current_stream().cuda_stream)
+    if stream is None:
+        with torch.cuda.device(device):
+            return body(torch.cuda.current_stream().cuda_stream)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _io_tensor(t, name, ndim, what):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {what}")
+    if t.dtype not in _IO_CODES:
+        raise TypeError(f"I/O tensors must be float32 or bfloat16, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError("libsscan works on CUDA tensors only")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.device, t.dtype
+
+
+def _scratch(need, workspace, device):
+    """(address, bytes) of the caller's workspace or a new one, and the tensor to keep alive."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _conv_args(u, weight, bias, ndim, silu):
+    dev, io = _io_tensor(u, "u", ndim, "(batch, L, D)" if ndim == 3 else "(batch, D)")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a (D, K) tensor")
+    D, K = u.shape[-1], weight.shape[1]
+    _expect(weight, "weight", (D, K), torch.float32, dev)
+    _expect(bias, "bias", (D,), torch.float32, dev)
+    L = u.shape[1] if ndim == 3 else 1
+    return dev, io, ConvProblem(u.shape[0], L, D, K, _IO_CODES[io], SSCAN_CONV_SILU if silu else 0)
+
+
+def sscan_conv_fwd(u, weight, bias=None, state0=None, *, silu=True, out=None, return_last_state=False, stream=None):
+    """Causal depthwise convolution (and SiLU) of u (batch, L, D) with weight (D, K) fp32, K = 2..4.
+    state0 (batch, K-1, D), in u's dtype, holds the inputs before the sequence.  Returns ``out``
+    or ``(out, state_last)``."""
+    dev, io, prob = _conv_args(u, weight, bias, 3, silu)
+    window = (prob.batch, max(prob.taps - 1, 0), prob.dim)
+    _expect(state0, "state0", window, io, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        y = torch.empty_like(u) if out is None else out
+        last = torch.empty(window, dtype=io, device=dev) if return_last_state else None
+        _check(load_library().sscan_conv_fwd(prob, _at(u), _at(weight), _at(bias), _at(state0), _at(y), _at(last), st))
+        return (y, last) if return_last_state else y
+    return _on(dev, stream, body)
+
+
+def sscan_conv_bwd(u, weight, dout, bias=None, state0=None, *, silu=True, want_dstate0=True, workspace=None,
+                   stream=None):
+    """Gradients of sum(out * dout) of sscan_conv_fwd: a dict keyed du, dweight and, when the
+    matching input is given, dbias and dstate0 (unless ``want_dstate0`` is false)."""
+    dev, io, prob = _conv_args(u, weight, bias, 3, silu)
+    _expect(state0, "state0", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
+    _require(dout, "dout")
+    _expect(dout, "dout", u.shape, io, dev)
+
+    def body(st):
+        lib = load_library()
+        g = {"du": torch.empty_like(u), "dweight": torch.empty_like(weight)}
+        if bias is not None:
+            g["dbias"] = torch.empty_like(bias)
+        if state0 is not None and want_dstate0:
+            g["dstate0"] = torch.empty_like(state0)
+        ws, nbytes, keep = _scratch(lib.sscan_conv_workspace_size(prob, SSCAN_OP_BWD), workspace, dev)
+        _check(lib.sscan_conv_bwd(prob, _at(u), _at(weight), _at(bias), _at(state0), _at(dout), _at(g["du"]),
+                                  _at(g["dweight"]), _at(g.get("dbias")), _at(g.get("dstate0")), ws, nbytes, st))
+        return g
+    return _on(dev, stream, body)
+
+
+def sscan_conv_step(u, weight, state, bias=None, *, silu=True, out=None, stream=None):
+    """One token: u (batch, D); state (batch, K-1, D) in u's dtype is shifted in place.  Returns
+    out (batch, D)."""
+    dev, io, prob = _conv_args(u, weight, bias, 2, silu)
+    _require(state, "state")
+    _expect(state, "state", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        y = torch.empty_like(u) if out is None else out
+        _check(load_library().sscan_conv_step(prob, _at(u), _at(weight), _at(bias), _at(state), _at(y), st))
+        return y
+    return _on(dev, stream, body)
+
+
+def _require(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+
+
+def _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, ndim, rate):
+    dev, io = _io_tensor(u, "u", ndim, "(batch, L, D)" if ndim == 3 else "(batch, D)")
+    for t, name in ((a_raw, "a_raw"), (i_raw, "i_raw"), (Lam, "Lam")):
+        _require(t, name)
+    D = u.shape[-1]
+    _expect(a_raw, "a_raw", u.shape, io, dev)
+    _expect(i_raw, "i_raw", u.shape, io, dev)
+    for t, name in ((Lam, "Lam"), (a_bias, "a_bias"), (i_bias, "i_bias")):
+        _expect(t, name, (D,), torch.float32, dev)
+    return dev, io, GatedProblem(u.shape[0], u.shape[1] if ndim == 3 else 1, D, _IO_CODES[io], rate)
+
+
+def sscan_gated_fwd(u, a_raw, i_raw, Lam, a_bias=None, i_bias=None, h0=None, *, rate=8.0, out=None,
+                    return_last_state=False, return_checkpoints=False, workspace=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_raw + i_bias) u_t with
+    a_t = exp(-rate softplus(Lam) sigmoid(a_raw + a_bias)): u, a_raw, i_raw (batch, L, D); Lam and
+    the biases (D) fp32; h0 (batch, D) fp32.  Returns ``out`` (the h_t), followed by h_last
+    (batch, D) and by the checkpoints that sscan_gated_bwd takes, where asked for."""
+    dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 3, rate)
+    _expect(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        lib = load_library()
+        f32 = dict(dtype=torch.float32, device=dev)
+        y = torch.empty_like(u) if out is None else out
+        last = torch.empty((prob.batch, prob.dim), **f32) if return_last_state else None
+        ck = torch.empty((prob.batch, lib.sscan_gated_checkpoints(prob), prob.dim), **f32) if return_checkpoints else None
+        ws, nbytes, keep = _scratch(lib.sscan_gated_workspace_size(prob, SSCAN_OP_FWD), workspace, dev)
+        _check(lib.sscan_gated_fwd(prob, _at(u), _at(a_raw), _at(i_raw), _at(Lam), _at(a_bias), _at(i_bias), _at(h0),
+                                   _at(y), _at(last), _at(ck), ws, nbytes, st))
+        r = (y,) + ((last,) if return_last_state else ()) + ((ck,) if return_checkpoints else ())
+        return r if len(r) > 1 else y
+    return _on(dev, stream, body)
+
+
+def sscan_gated_bwd(u, a_raw, i_raw, Lam, dout, a_bias=None, i_bias=None, h0=None, *, rate=8.0, checkpoints=None,
+                    want_dh0=True, workspace=None, stream=None):
+    """Gradients of sum(out * dout) of sscan_gated_fwd on the same inputs: a dict keyed du, da_raw,
+    di_raw, dLam, da_bias and di_bias when that bias is given, and dh0 when ``want_dh0``.
+    ``checkpoints``: what sscan_gated_fwd saved (else a pass over the inputs rebuilds them)."""
+    dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 3, rate)
+    _require(dout, "dout")
+    _expect(dout, "dout", u.shape, io, dev)
+    _expect(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
+    if checkpoints is not None:
+        _expect(checkpoints, "checkpoints", (prob.batch, load_library().sscan_gated_checkpoints(prob), prob.dim),
+                torch.float32, dev)
+
+    def body(st):
+        lib = load_library()
+        g = {k: torch.empty_like(u) for k in ("du", "da_raw", "di_raw")}
+        g["dLam"] = torch.empty_like(Lam)
+        if a_bias is not None:
+            g["da_bias"] = torch.empty_like(a_bias)
+        if i_bias is not None:
+            g["di_bias"] = torch.empty_like(i_bias)
+        if want_dh0:
+            g["dh0"] = torch.empty((prob.batch, prob.dim), dtype=torch.float32, device=dev)
+        ws, nbytes, keep = _scratch(lib.sscan_gated_workspace_size(prob, SSCAN_OP_BWD), workspace, dev)
+        _check(lib.sscan_gated_bwd(prob, _at(u), _at(a_raw), _at(i_raw), _at(Lam), _at(a_bias), _at(i_bias), _at(h0),
+                                   _at(checkpoints), _at(dout), _at(g["du"]), _at(g["da_raw"]), _at(g["di_raw"]),
+                                   _at(g["dLam"]), _at(g.get("da_bias")), _at(g.get("di_bias")), _at(g.get("dh0")),
+                                   ws, nbytes, st))
+        return g
+    return _on(dev, stream, body)
+
+
+def sscan_gated_step(u, a_raw, i_raw, Lam, state, a_bias=None, i_bias=None, *, rate=8.0, out=None, stream=None):
+    """One token: u, a_raw, i_raw (batch, D); state (batch, D) fp32 updated in place.  Returns out
+    (batch, D), the new state rounded to u's dtype."""
+    dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 2, rate)
+    _require(state, "state")
+    _expect(state, "state", u.shape, torch.float32, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        y = torch.empty_like(u) if out is None else out
+        _check(load_library().sscan_gated_step(prob, _at(u), _at(a_raw), _at(i_raw), _at(Lam), _at(a_bias), _at(i_bias),
+                                               _at(state), _at(y), st))
+        return y
+    return _on(dev, stream, body)
 
 
 def device_status(clear: bool = False) -> int:

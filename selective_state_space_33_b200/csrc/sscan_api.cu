@@ -10,6 +10,7 @@
 #include "sscan.h"
 #include "sscan_generic.cuh"
 #include "sscan_generic_bwd.cuh"
+#include "sscan_host.h"
 #include "sscan_launch.h"
 #include "sscan_plan.h"
 
@@ -320,6 +321,38 @@ sscan_status noalloc_scratch(void** ptr) {
 }
 
 }  // namespace
+
+namespace sscan {
+
+void api_begin() {
+    g_err[0] = 0;
+    g_launches = 0;
+}
+
+sscan_status api_fail(sscan_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+void api_count_launch() { ++g_launches; }
+
+sscan_status api_launched(const char* what) { return cuda_check(what); }
+
+sscan_status api_workspace(size_t need, const void* ws, size_t bytes) { return check_workspace(need, ws, bytes); }
+
+sscan_status api_elements(int64_t batch, int64_t L, int64_t D) {
+    const int64_t most = int64_t(1) << 37;
+    if (batch > most || L > most || D > most || (batch > 0 && D > most / batch) ||
+        (batch * D > 0 && L > most / (batch * D)))
+        return fail(SSCAN_ERR_UNSUPPORTED, "more than 2^37 elements (%lld x %lld x %lld)", (long long)batch,
+                    (long long)L, (long long)D);
+    return SSCAN_OK;
+}
+
+}  // namespace sscan
 
 extern "C" {
 
@@ -850,12 +883,13 @@ int sscan_debug_bounds(void) {
 sscan_status sscan_device_status(int clear, unsigned int* flags) {
     g_err[0] = 0;
     if (!flags) return fail(SSCAN_ERR_INVALID_ARG, "flags is NULL");
-    unsigned int f1 = 0, f2 = 0, f3 = 0;
+    unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0;
     cudaError_t e = sscan::read_device_error(&f1, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_bwd(&f2, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_cx(&f3, clear);
+    if (e == cudaSuccess) e = sscan::read_device_error_gated(&f4, clear);
     if (e != cudaSuccess) return fail(SSCAN_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(e));
-    *flags = f1 | f2 | f3;
+    *flags = f1 | f2 | f3 | f4;
     return *flags ? SSCAN_ERR_TIMEOUT : SSCAN_OK;
 }
 

@@ -169,6 +169,10 @@ cudaError_t read_device_error_bwd(unsigned int* value, int clear);
 // bounded wait in a kernel gave up.  Synchronous.
 cudaError_t read_device_error(unsigned int* value, int clear);
 
+// The gated recurrence's error word (bits 0 and 1: a bounded wait for an earlier tile's
+// carry gave up in the forward / backward kernel).  Synchronous.
+cudaError_t read_device_error_gated(unsigned int* value, int clear);
+
 // One thread waits, with the kernels' bounded wait cut to `polls` polls, on an
 // mbarrier that nothing arrives on, then raises bit 2 of the device error word.
 cudaError_t launch_wait_probe(unsigned int polls, cudaStream_t st);
