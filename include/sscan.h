@@ -350,6 +350,57 @@ SSCAN_API sscan_status sscan_gated_step(const sscan_gated_problem* problem, cons
                                         const void* i_raw, const float* Lam, const float* a_bias,
                                         const float* i_bias, float* state, void* out, void* stream);
 
+/*
+ * Multi-head linear recurrence with a P x N state per head and one decay per head and token
+ * (the selective scan whose A is a scalar per head, so that the sequence can be taken in
+ * chunks of matrix products).  Per batch row b and head h, group g = h / (heads / groups):
+ *   delta_t = softplus(delta_raw_t + delta_bias_h)   (SSCAN_DELTA_SOFTPLUS, else the sum)
+ *   S_t = exp(delta_t A_h) S_{t-1} + expm1(delta_t A_h) / A_h  u_t B_tg^T
+ *                                                    (delta_t in place of the fraction at A_h = 0)
+ *   y_t = S_t C_tg + D_skip_h u_t,   out_t = y_t * SiLU(z_t)   (when z is given)
+ * u, z, out (batch, L, heads, headdim), delta_raw (batch, L, heads), B, C (batch, L, groups,
+ * dstate) in io_dtype; A, delta_bias, D_skip (heads) and h0, h_last (batch, heads, headdim,
+ * dstate) fp32.  delta_bias, D_skip, z, h0, h_last may be NULL.
+ */
+typedef struct sscan_heads_problem {
+    int64_t batch;    /* 0 .. 65535 */
+    int64_t seqlen;   /* L >= 0 */
+    int64_t heads;    /* >= 0, a multiple of groups */
+    int64_t headdim;  /* P, 1..64 */
+    int64_t dstate;   /* N, 1..128 */
+    int64_t groups;   /* >= 1: heads that share their B and C */
+    int32_t io_dtype; /* sscan_dtype of the (batch, L, ...) tensors */
+    uint32_t flags;   /* SSCAN_DELTA_SOFTPLUS or 0 */
+} sscan_heads_problem;
+
+/* Bytes of workspace for op SSCAN_OP_FWD or SSCAN_OP_BWD (0 when none). */
+SSCAN_API size_t sscan_heads_workspace_size(const sscan_heads_problem* problem, int op);
+
+/* Steps are taken 64 at a time; a value that is not finite reaches only its own and later
+ * steps, as in the recurrence. */
+SSCAN_API sscan_status sscan_heads_fwd(const sscan_heads_problem* problem, const void* u, const void* delta_raw,
+                                       const float* delta_bias, const float* A, const void* B, const void* C,
+                                       const float* D_skip, const void* z, const float* h0, void* out,
+                                       float* h_last, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out * dout).  du, ddelta_raw, dB, dC, dz in io_dtype (dB, dC summed over
+ * the heads of a group); dA, ddelta_bias, dD (heads) and dh0 fp32.  ddelta_bias, dD, dz and
+ * dh0 may be NULL; dz is given exactly when z is, ddelta_bias and dD only with their input.
+ * A value that is not finite may reach every gradient of its 64-step chunk. */
+SSCAN_API sscan_status sscan_heads_bwd(const sscan_heads_problem* problem, const void* u, const void* delta_raw,
+                                       const float* delta_bias, const float* A, const void* B, const void* C,
+                                       const float* D_skip, const void* z, const float* h0, const void* dout,
+                                       void* du, void* ddelta_raw, float* ddelta_bias, float* dA, void* dB, void* dC,
+                                       float* dD, void* dz, float* dh0, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* One token: problem->seqlen must be 1; u, z, out (batch, heads, headdim), delta_raw (batch,
+ * heads), B, C (batch, groups, dstate); state (batch, heads, headdim, dstate) fp32 is read and
+ * overwritten in place. */
+SSCAN_API sscan_status sscan_heads_step(const sscan_heads_problem* problem, const void* u, const void* delta_raw,
+                                        const float* delta_bias, const float* A, const void* B, const void* C,
+                                        const float* D_skip, const void* z, float* state, void* out, void* stream);
+
 /* One-line reason for the most recent failed call on this thread ("" if none). */
 SSCAN_API const char* sscan_last_error(void);
 

@@ -50,6 +50,12 @@ class GatedProblem(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("rate", ctypes.c_float)]
 
 
+class HeadsProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libsscan.so (built in-tree by ``selective_state_space_33_b200/build.py``)."""
     global _lib
@@ -92,7 +98,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sscan_gated_fwd.argtypes = [gp] + [vp] * 11 + [sz, vp]
     lib.sscan_gated_bwd.argtypes = [gp] + [vp] * 17 + [sz, vp]
     lib.sscan_gated_step.argtypes = [gp] + [vp] * 8 + [vp]
-    for f in ("conv_fwd", "conv_bwd", "conv_step", "gated_fwd", "gated_bwd", "gated_step"):
+    hp = ctypes.POINTER(HeadsProblem)
+    lib.sscan_heads_workspace_size.argtypes = [hp, ctypes.c_int]
+    lib.sscan_heads_workspace_size.restype = sz
+    lib.sscan_heads_fwd.argtypes = [hp] + [vp] * 12 + [sz, vp]
+    lib.sscan_heads_bwd.argtypes = [hp] + [vp] * 20 + [sz, vp]
+    lib.sscan_heads_step.argtypes = [hp] + [vp] * 10 + [vp]
+    for f in ("conv_fwd", "conv_bwd", "conv_step", "gated_fwd", "gated_bwd", "gated_step", "heads_fwd", "heads_bwd",
+              "heads_step"):
         getattr(lib, "sscan_" + f).restype = ctypes.c_int
     lib.sscan_status_string.argtypes = [ctypes.c_int]
     lib.sscan_status_string.restype = ctypes.c_char_p
@@ -591,6 +604,89 @@ def sscan_gated_step(u, a_raw, i_raw, Lam, state, a_bias=None, i_bias=None, *, r
         y = torch.empty_like(u) if out is None else out
         _check(load_library().sscan_gated_step(prob, _at(u), _at(a_raw), _at(i_raw), _at(Lam), _at(a_bias), _at(i_bias),
                                                _at(state), _at(y), st))
+        return y
+    return _on(dev, stream, body)
+
+
+def _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, ndim, delta_softplus):
+    dev, io = _io_tensor(u, "u", ndim, "(batch, L, heads, P)" if ndim == 4 else "(batch, heads, P)")
+    for t, name in ((delta_raw, "delta_raw"), (A, "A"), (B, "B"), (C, "C")):
+        _require(t, name)
+    if not isinstance(B, torch.Tensor) or B.dim() != ndim:
+        raise ValueError("B must be (batch, L, groups, N)" if ndim == 4 else "B must be (batch, groups, N)")
+    lead, H, P = tuple(u.shape[:-2]), u.shape[-2], u.shape[-1]
+    G, N = B.shape[-2], B.shape[-1]
+    _expect(delta_raw, "delta_raw", lead + (H,), io, dev)
+    _expect(z, "z", u.shape, io, dev)
+    _expect(B, "B", lead + (G, N), io, dev)
+    _expect(C, "C", lead + (G, N), io, dev)
+    for t, name in ((A, "A"), (delta_bias, "delta_bias"), (D_skip, "D_skip")):
+        _expect(t, name, (H,), torch.float32, dev)
+    return dev, io, HeadsProblem(lead[0], lead[1] if ndim == 4 else 1, H, P, N, G, _IO_CODES[io],
+                                 SSCAN_DELTA_SOFTPLUS if delta_softplus else 0)
+
+
+def sscan_heads_fwd(u, delta_raw, A, B, C, delta_bias=None, D_skip=None, z=None, h0=None, *, delta_softplus=True,
+                    out=None, return_last_state=False, workspace=None, stream=None):
+    """Multi-head linear recurrence with a P x N state per head (the selective scan whose A is a
+    scalar per head): u, z (batch, L, heads, P), P <= 64; delta_raw (batch, L, heads); B, C
+    (batch, L, groups, N), N <= 128, shared by heads / groups heads each; A, delta_bias, D_skip
+    (heads) fp32; h0 (batch, heads, P, N) fp32.  Returns ``out`` or ``(out, h_last)``."""
+    dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 4, delta_softplus)
+    state = (prob.batch, prob.heads, prob.headdim, prob.dstate)
+    _expect(h0, "h0", state, torch.float32, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        lib = load_library()
+        y = torch.empty_like(u) if out is None else out
+        last = torch.empty(state, dtype=torch.float32, device=dev) if return_last_state else None
+        ws, nbytes, keep = _scratch(lib.sscan_heads_workspace_size(prob, SSCAN_OP_FWD), workspace, dev)
+        _check(lib.sscan_heads_fwd(prob, _at(u), _at(delta_raw), _at(delta_bias), _at(A), _at(B), _at(C), _at(D_skip),
+                                   _at(z), _at(h0), _at(y), _at(last), ws, nbytes, st))
+        return (y, last) if return_last_state else y
+    return _on(dev, stream, body)
+
+
+def sscan_heads_bwd(u, delta_raw, A, B, C, dout, delta_bias=None, D_skip=None, z=None, h0=None, *,
+                    delta_softplus=True, want_dh0=True, workspace=None, stream=None):
+    """Gradients of sum(out * dout) of sscan_heads_fwd: a dict keyed du, ddelta_raw, dA, dB, dC and,
+    when the matching input is given, ddelta_bias, dD, dz; dh0 when ``want_dh0``."""
+    dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 4, delta_softplus)
+    state = (prob.batch, prob.heads, prob.headdim, prob.dstate)
+    _require(dout, "dout")
+    _expect(dout, "dout", u.shape, io, dev)
+    _expect(h0, "h0", state, torch.float32, dev)
+
+    def body(st):
+        lib = load_library()
+        like = {"du": u, "ddelta_raw": delta_raw, "ddelta_bias": delta_bias, "dA": A, "dB": B, "dC": C, "dD": D_skip,
+                "dz": z}
+        g = {k: torch.empty_like(t) for k, t in like.items() if t is not None}
+        if want_dh0:
+            g["dh0"] = torch.empty(state, dtype=torch.float32, device=dev)
+        ws, nbytes, keep = _scratch(lib.sscan_heads_workspace_size(prob, SSCAN_OP_BWD), workspace, dev)
+        _check(lib.sscan_heads_bwd(prob, _at(u), _at(delta_raw), _at(delta_bias), _at(A), _at(B), _at(C), _at(D_skip),
+                                   _at(z), _at(h0), _at(dout), _at(g["du"]), _at(g["ddelta_raw"]),
+                                   _at(g.get("ddelta_bias")), _at(g["dA"]), _at(g["dB"]), _at(g["dC"]),
+                                   _at(g.get("dD")), _at(g.get("dz")), _at(g.get("dh0")), ws, nbytes, st))
+        return g
+    return _on(dev, stream, body)
+
+
+def sscan_heads_step(u, delta_raw, A, B, C, state, delta_bias=None, D_skip=None, z=None, *, delta_softplus=True,
+                     out=None, stream=None):
+    """One token: u, z (batch, heads, P); delta_raw (batch, heads); B, C (batch, groups, N); state
+    (batch, heads, P, N) fp32 updated in place.  Returns out (batch, heads, P)."""
+    dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 3, delta_softplus)
+    _require(state, "state")
+    _expect(state, "state", (prob.batch, prob.heads, prob.headdim, prob.dstate), torch.float32, dev)
+    _expect(out, "out", u.shape, io, dev)
+
+    def body(st):
+        y = torch.empty_like(u) if out is None else out
+        _check(load_library().sscan_heads_step(prob, _at(u), _at(delta_raw), _at(delta_bias), _at(A), _at(B), _at(C),
+                                               _at(D_skip), _at(z), _at(state), _at(y), st))
         return y
     return _on(dev, stream, body)
 

@@ -1,0 +1,155 @@
+// sscan_heads.cuh -- what the forward and backward kernels of the multi-head recurrence share.
+//
+// Per batch row and head, with dl = softplus(delta_raw + bias), q = dl A, w = expm1(q) / A:
+//   S_t = exp(q_t) S_{t-1} + w_t u_t B_t^T   (P x N),    y_t = S_t C_t + D u_t,
+//   out_t = y_t SiLU(z_t).
+// A chunk of kQ steps, with c_t the running sum of q from the chunk's start and S the state
+// entering it, is three matrix products:
+//   Y = M U + exp(c) C S^T,   M_ts = (C_t . B_s) exp(c_t - c_s) w_s for s <= t, else 0,
+//   S' = exp(c_end) S + (f U)^T B,   f_s = exp(c_end - c_s) w_s.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "sscan_host.h"
+#include "sscan_math.cuh"
+#include "sscan_mma.cuh"
+#include "sscan_tma.cuh"
+
+namespace sscan {
+
+constexpr int kQ = 64;        // steps per chunk
+constexpr int kHeadDim = 64;  // a head's channels in a tile (fewer are padded with zeros)
+
+struct HeadsArgs {
+    int64_t batch, L;
+    int H, P, N, G;
+    int softplus;
+    int vec;                  // rows of u, z, dout and of B, C start and end on 16-byte boundaries
+    const void *u, *delta_raw, *B, *C, *z;
+    const float *A, *bias, *D, *h0;
+    void* out;
+    float* h_last;
+    int64_t chunks;           // ceil(L / kQ)
+    // sequence split into segments of seg_chunks chunks
+    int64_t seg_chunks, nseg;
+    float* states;            // [batch][H][nseg][P][N]: segment end states, then entering states
+    float* decays;            // [batch][H][nseg]: sum of q over the segment
+};
+
+// Scalars of one chunk's steps, and their running sums.
+struct ChunkScalars {
+    float ch[kQ], cl[kQ];     // log2(e) c_t as the sum of two floats: the difference of two of
+                              // them keeps its absolute error near 2^-24 whatever c_t's size
+    float w[kQ];
+    float e[kQ];              // exp(c_t)
+    float d[kQ];              // exp(c_end - c_t)
+    float f[kQ];              // d_t w_t
+    float dl[kQ], raw[kQ];    // step sizes, and what softplus was taken of
+    float total;              // c_end
+};
+
+// One warp fills s for steps t0 .. t0 + kQ - 1 of (b, h); past L: q = w = 0.
+template <typename T>
+__device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& a, int64_t b, int h, int64_t t0) {
+    const int lane = threadIdx.x & 31;
+    const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
+    const T* dr = static_cast<const T*>(a.delta_raw);
+    double c[2];
+    float w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t t = t0 + 2 * lane + i;
+        c[i] = 0.0;
+        w[i] = 0.f;
+        s.dl[2 * lane + i] = s.raw[2 * lane + i] = 0.f;
+        if (t < a.L) {
+            const float r = IO<T>::load(dr, (b * a.L + t) * a.H + h) + bias;
+            const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
+            const float q = dl * A;
+            w[i] = A != 0.f ? expm1f(q) / A : dl;
+            c[i] = q < -1e4f ? -1e4 : (double)q;  // exp(-1e4) is 0 in fp32; keeps sums finite
+            s.dl[2 * lane + i] = dl;
+            s.raw[2 * lane + i] = r;
+        }
+    }
+    c[1] += c[0];
+    double run = c[1];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const double v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+    }
+    const double before = run - c[1], end = __shfl_sync(0xffffffffu, run, 31);
+    constexpr double l2e = 1.4426950408889634074;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const double ct = (before + c[i]) * l2e;
+        s.ch[t] = (float)ct;
+        s.cl[t] = (float)(ct - (double)s.ch[t]);
+        s.w[t] = w[i];
+        s.e[t] = ex2((float)ct);
+        s.d[t] = ex2((float)(end * l2e - ct));
+        s.f[t] = s.d[t] * w[i];
+    }
+    if (lane == 0) s.total = (float)end;
+}
+
+// exp(c_t - c_s)
+__device__ __forceinline__ float chunk_decay(const ChunkScalars& s, int t, int u) {
+    return ex2((s.ch[t] - s.ch[u]) + (s.cl[t] - s.cl[u]));
+}
+
+// rows x COLS tile of T from global rows (`stride` elements apart) into shared memory, zeros
+// past `rows` and `cols`.  vec: every row starts on a 16-byte boundary and cols is a multiple
+// of 16 bytes.
+template <typename T, int COLS>
+__device__ __forceinline__ void load_tile(T* dst, int pitch, const T* src, int64_t stride, int64_t rows, int cols,
+                                          bool vec, int tid, int threads) {
+    constexpr int VE = 16 / sizeof(T), PER = COLS / VE;
+    for (int i = tid; i < kQ * PER; i += threads) {
+        const int r = i / PER, c = (i - r * PER) * VE;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows && c < cols) {
+            const T* p = src + r * stride + c;
+            if (vec) {
+                v = __ldg(reinterpret_cast<const uint4*>(p));
+            } else {
+                T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+                for (int j = 0; j < VE; ++j)
+                    if (c + j < cols) e[j] = p[j];
+            }
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = v;
+    }
+}
+
+// x as hi + lo in the tile type: bf16 keeps 16 bits in the two (a relative 2^-17), which is
+// what an fp32 state or gradient needs from a factor that is not itself a bf16 input; an
+// fp32 tile needs no second part.
+template <typename T>
+__device__ __forceinline__ void split_store(T* hi, T* lo, int at, float x) {
+    const T h = from_f32<T>(x);
+    hi[at] = h;
+    if constexpr (!Mma<T>::kExact32) lo[at] = from_f32<T>(x - to_f32<T>(h));
+}
+
+template <typename T, int NT> struct HeadsPitch {
+    static constexpr int P = kHeadDim + Mma<T>::PAD;
+    static constexpr int N = NT + Mma<T>::PAD;
+    static constexpr int Q = kQ + Mma<T>::PAD;
+};
+
+// Segment end states from zero (forward: of S; reverse: of its adjoint), and the carry
+// through them; sscan_heads.cu.
+void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, float* last, cudaStream_t st);
+sscan_status check_heads(const sscan_heads_problem* p);
+HeadsArgs heads_args(const sscan_heads_problem* p, const void* u, const void* delta_raw, const float* delta_bias,
+                     const float* A, const void* B, const void* C, const float* D_skip, const void* z,
+                     const float* h0);
+// Local states of every segment: forward (u, B) or, with dout, reverse (dout SiLU(z), C).
+cudaError_t launch_heads_local(const HeadsArgs& a, const void* dout, bool bf16, cudaStream_t st);
+
+}  // namespace sscan

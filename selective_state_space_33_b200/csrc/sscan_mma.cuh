@@ -1,0 +1,176 @@
+// sscan_mma.cuh -- warp-level matrix products over shared-memory tiles for the multi-head
+// recurrence: one interface over bf16 operands and over fp32 operands, accumulating in fp32.
+//
+// Element (row, k) of A and (k, col) of B come from row-major tiles, either as stored or
+// transposed.  bf16: m16n8k16 instructions, fragments by ldmatrix.  fp32: m16n8k8 tf32
+// instructions on operands split in two tf32 parts, x = hi + lo with |lo| <= 2^-11 |x|; the
+// three products hi hi, hi lo, lo hi leave out lo lo, a relative 2^-22.  The k slots of an
+// fp32 fragment are permuted (slot t holds k = 2t, slot t + 4 holds k = 2t + 1) so that an
+// accumulator is an A fragment as it stands.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace sscan {
+
+template <typename T> struct Mma;
+
+template <> struct Mma<__nv_bfloat16> {
+    using T = __nv_bfloat16;
+    static constexpr int KS = 16;   // k per instruction
+    static constexpr int KT = 2;    // 8-wide accumulator tiles per A fragment
+    static constexpr int PAD = 8;   // elements added to a tile's row pitch: 16 bytes, so that eight
+                                    // consecutive rows start in eight different 16-byte bank groups
+    static constexpr bool kExact32 = false;
+    struct A { uint32_t r[4]; };
+    struct B { uint32_t r[2]; };
+
+    static __device__ __forceinline__ uint32_t addr(const T* p) {
+        return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    }
+    // rows m0 .. m0+15, k0 .. k0+15 of a tile stored [m][k]
+    static __device__ __forceinline__ void load_a(A& a, const T* s, int pitch, int m0, int k0) {
+        const int l = threadIdx.x & 31;
+        const uint32_t p = addr(s + (m0 + (l & 15)) * pitch + k0 + (l >> 4) * 8);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(a.r[0]), "=r"(a.r[1]), "=r"(a.r[2]), "=r"(a.r[3]) : "r"(p) : "memory");
+    }
+    // the same from a tile stored [k][m]
+    static __device__ __forceinline__ void load_at(A& a, const T* s, int pitch, int m0, int k0) {
+        const int l = threadIdx.x & 31;
+        const uint32_t p = addr(s + (k0 + (l & 7) + (l >> 4) * 8) * pitch + m0 + ((l >> 3) & 1) * 8);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(a.r[0]), "=r"(a.r[1]), "=r"(a.r[2]), "=r"(a.r[3]) : "r"(p) : "memory");
+    }
+    // columns n0 .. n0+15 (two fragments), k0 .. k0+15 of a tile stored [n][k]
+    static __device__ __forceinline__ void load_b2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+        const int l = threadIdx.x & 31;
+        const uint32_t p = addr(s + (n0 + (l & 7) + (l >> 4) * 8) * pitch + k0 + ((l >> 3) & 1) * 8);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(b0.r[0]), "=r"(b0.r[1]), "=r"(b1.r[0]), "=r"(b1.r[1]) : "r"(p) : "memory");
+    }
+    // the same from a tile stored [k][n]
+    static __device__ __forceinline__ void load_bt2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+        const int l = threadIdx.x & 31;
+        const uint32_t p = addr(s + (k0 + (l & 15)) * pitch + n0 + (l >> 4) * 8);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(b0.r[0]), "=r"(b0.r[1]), "=r"(b1.r[0]), "=r"(b1.r[1]) : "r"(p) : "memory");
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    // accumulator tiles c[0], c[1] (16 rows by 16 columns) as an A fragment, rounded to bf16
+    static __device__ __forceinline__ void from_acc(A& a, const float (*c)[4]) {
+        a.r[0] = pack(c[0][0], c[0][1]);
+        a.r[1] = pack(c[0][2], c[0][3]);
+        a.r[2] = pack(c[1][0], c[1][1]);
+        a.r[3] = pack(c[1][2], c[1][3]);
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const A& a, const B& b) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a.r[0]), "r"(a.r[1]), "r"(a.r[2]), "r"(a.r[3]), "r"(b.r[0]), "r"(b.r[1]));
+    }
+};
+
+template <> struct Mma<float> {
+    using T = float;
+    static constexpr int KS = 8;
+    static constexpr int KT = 1;
+    static constexpr int PAD = 4;
+    static constexpr bool kExact32 = true;
+    struct A { uint32_t hi[4], lo[4]; };
+    struct B { uint32_t hi[2], lo[2]; };
+
+    static __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+        const float rest = x - __uint_as_float(hi);
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+    }
+    static __device__ __forceinline__ void put(A& a, int i, float x) { split(x, a.hi[i], a.lo[i]); }
+    static __device__ __forceinline__ void load_a(A& a, const T* s, int pitch, int m0, int k0) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        const float* p = s + (m0 + g) * pitch + k0 + 2 * t;
+        put(a, 0, p[0]);
+        put(a, 1, p[8 * pitch]);
+        put(a, 2, p[1]);
+        put(a, 3, p[8 * pitch + 1]);
+    }
+    static __device__ __forceinline__ void load_at(A& a, const T* s, int pitch, int m0, int k0) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        const float* p = s + (k0 + 2 * t) * pitch + m0 + g;
+        put(a, 0, p[0]);
+        put(a, 1, p[8]);
+        put(a, 2, p[pitch]);
+        put(a, 3, p[pitch + 8]);
+    }
+    static __device__ __forceinline__ void load_b(B& b, const T* s, int pitch, int n0, int k0) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        const float* p = s + (n0 + g) * pitch + k0 + 2 * t;
+        split(p[0], b.hi[0], b.lo[0]);
+        split(p[1], b.hi[1], b.lo[1]);
+    }
+    static __device__ __forceinline__ void load_bt(B& b, const T* s, int pitch, int n0, int k0) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        const float* p = s + (k0 + 2 * t) * pitch + n0 + g;
+        split(p[0], b.hi[0], b.lo[0]);
+        split(p[pitch], b.hi[1], b.lo[1]);
+    }
+    static __device__ __forceinline__ void load_b2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+        load_b(b0, s, pitch, n0, k0);
+        load_b(b1, s, pitch, n0 + 8, k0);
+    }
+    static __device__ __forceinline__ void load_bt2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+        load_bt(b0, s, pitch, n0, k0);
+        load_bt(b1, s, pitch, n0 + 8, k0);
+    }
+    static __device__ __forceinline__ void from_acc(A& a, const float (*c)[4]) {
+        put(a, 0, c[0][0]);
+        put(a, 1, c[0][2]);
+        put(a, 2, c[0][1]);
+        put(a, 3, c[0][3]);
+    }
+    static __device__ __forceinline__ void one(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], const A& a, const B& b) {
+        one(c, a.lo, b.hi);
+        one(c, a.hi, b.lo);
+        one(c, a.hi, b.hi);
+    }
+};
+
+// acc[NTL][4] (16 rows m0.. by 8 NTL columns n0..) += A[m][k] B[k][n], k = 0 .. K-1.
+// AT / BT: the operand's tile is stored [k][m] / [k][n] instead of [m][k] / [n][k].  NTL is even.
+template <typename T, bool AT, bool BT, int NTL>
+__device__ __forceinline__ void warp_gemm(float (&acc)[NTL][4], const T* A, int pa, int m0, const T* B, int pb, int n0,
+                                          int k_begin, int k_end) {
+    using M = Mma<T>;
+#pragma unroll 2
+    for (int k = k_begin; k < k_end; k += M::KS) {
+        typename M::A a;
+        if constexpr (AT) M::load_at(a, A, pa, m0, k);
+        else M::load_a(a, A, pa, m0, k);
+#pragma unroll
+        for (int j = 0; j < NTL; j += 2) {
+            typename M::B b0, b1;
+            if constexpr (BT) M::load_bt2(b0, b1, B, pb, n0 + 8 * j, k);
+            else M::load_b2(b0, b1, B, pb, n0 + 8 * j, k);
+            M::mma(acc[j], a, b0);
+            M::mma(acc[j + 1], a, b1);
+        }
+    }
+}
+
+template <int NTL>
+__device__ __forceinline__ void zero_acc(float (&acc)[NTL][4]) {
+#pragma unroll
+    for (int j = 0; j < NTL; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+}
+
+}  // namespace sscan
