@@ -3,10 +3,13 @@
 // one-token step.
 //
 // heads_walk_kernel: one block per (head, batch row, segment) walks its chunks with the state
-// in the accumulators of its four warps (16 channels each), so a sequence that is not split
-// is read once.  In bf16 the factors that carry fp32 quantities into a product (the state, and
-// u scaled by f) go in as two bf16 parts; the entries of M are rounded to bf16 once, an error
-// of the same size as the rounding of the result.
+// in the accumulators of its warps, so a sequence that is not split is read once.  The next
+// chunk's tiles arrive by cp.async, and a warp of its own works out the next chunk's
+// scalars (exponentials and a running sum in fp64: a long chain of dependent operations),
+// while the other warps run the products of this chunk.  In bf16 the factor that carries an
+// fp32 quantity into the state (u or B scaled by f) goes in as three bf16 parts, the state
+// read by the outputs as two, and the entries of M are rounded to bf16 once, an error of the
+// same size as the rounding of the result.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -17,177 +20,337 @@
 namespace sscan {
 namespace {
 
-constexpr int kThreads = 128;
-
 enum { kWalkOut = 0, kWalkLocal = 1, kWalkLocalRev = 2 };
 
 template <typename T, int NT, int MODE>
-struct WalkSmem {
-    using Pt = HeadsPitch<T, NT>;
-    static constexpr bool two = !Mma<T>::kExact32, out = MODE == kWalkOut;
-    alignas(16) T x[kQ * Pt::P];                            // u (reverse: dout)
-    alignas(16) T fh[kQ * Pt::P];                           // its scaled copy, and the second part
-    alignas(16) T fl[two ? kQ * Pt::P : 1];
-    alignas(16) T B[kQ * Pt::N];                            // B (reverse: C)
-    alignas(16) T C[out ? kQ * Pt::N : 1];
-    alignas(16) T sh[out ? kHeadDim * Pt::N : 1];           // the state, [p][n]
-    alignas(16) T sl[out && two ? kHeadDim * Pt::N : 1];
-    ChunkScalars s;
+struct Walk {
+    static constexpr bool out = MODE == kWalkOut, bf16 = !Mma<T>::kExact32;
+    // 128 states: two warps share 16 rows, each with half of the columns, which halves the
+    // accumulators a warp holds
+    static constexpr int WC = NT == 128 ? 2 : 1;
+    static constexpr int NW = 4 * WC, threads = 32 * (NW + 1);
+    // blocks per SM that shared memory allows, and registers are held to
+    static constexpr int blocks = NT <= 32 ? 3 : bf16 || NT == 64 ? 2 : 1;
+    // two buffers of tiles where three blocks or more still fit an SM
+    static constexpr int stages = bf16 && NT <= 64 ? 2 : 1;
+    // up to 32 states B is the smaller factor to scale, once per block through shared memory;
+    // above, each warp scales its own 16 channels of u in registers
+    static constexpr bool scale_b = bf16 && out && NT <= 32;
+    static constexpr int PITCH_P = kHeadDim + Mma<T>::PAD, PITCH_N = NT + Mma<T>::PAD;
+
+    struct Tiles {
+        alignas(16) T x[kQ * PITCH_P];                       // u (reverse: dout)
+        alignas(16) T B[kQ * PITCH_N];                       // B (reverse: C)
+        alignas(16) T C[out ? kQ * PITCH_N : 8];
+        alignas(16) T zr[MODE == kWalkLocalRev ? kQ * PITCH_P : 8];
+    };
+    struct Smem {
+        Tiles t[stages];
+        alignas(16) T z[out ? kQ * PITCH_P : 8];             // the gate, then the outputs
+        alignas(16) T sh[out ? kHeadDim * PITCH_N : 8];      // the state, [p][n]
+        alignas(16) T sl[out && bf16 ? kHeadDim * PITCH_N : 8];
+        alignas(16) T fb[scale_b ? 3 : 1][scale_b ? kQ * PITCH_N : 8];  // f B in three parts
+        ChunkScalars s[2];
+    };
 };
 
-template <typename T, int NT, int MODE>
-__global__ void __launch_bounds__(kThreads) heads_walk_kernel(HeadsArgs a, const T* dout) {
-    using Pt = HeadsPitch<T, NT>;
+// barrier of the warps that run products (the scalars' warp stays out of it)
+template <int THREADS>
+__device__ __forceinline__ void product_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// The terms M_ts u_s, s <= t, of channel p whose u_s is not finite.
+template <typename T>
+__device__ __noinline__ float not_finite_terms(const T* C, const T* B, const T* x, const ChunkScalars& sc, int pn,
+                                               int pp, int N, int t, int p) {
+    float v = 0.f;
+    for (int s = 0; s <= t; ++s) {
+        const float xs = to_f32<T>(x[s * pp + p]);
+        if (fabsf(xs) <= 3.4e38f) continue;
+        float dot = 0.f;
+        for (int m = 0; m < N; ++m) dot = fmaf(to_f32<T>(C[t * pn + m]), to_f32<T>(B[s * pn + m]), dot);
+        v += dot * (chunk_decay(sc, t, s) * sc.w[s]) * xs;
+    }
+    return v;
+}
+
+// y = exp(c) C S^T + M U for 16 steps from t0 and 8 PTL channels from p0 of a chunk, the 16 columns
+// s of M at a time, up to the diagonal.  FINITE: elements of U that are not finite count as 0.
+template <typename T, int NT, int PTL, bool FINITE>
+__device__ __forceinline__ void chunk_outputs(float (&y)[PTL][4], const T* C, const T* B, const T* x, const T* sh,
+                                              const T* sl, const ChunkScalars& sc, int t0, int p0) {
     using M = Mma<T>;
-    constexpr int NTL = NT / 8, PTL = kHeadDim / 8;
+    constexpr int PP = kHeadDim + M::PAD, PN = NT + M::PAD;
+    const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3, ta = t0 + g, tb = ta + 8;
+    zero_acc(y);
+    warp_gemm<T, false, false, PTL>(y, C, PN, t0, sh, PN, p0, 0, NT);
+    if constexpr (!M::kExact32) warp_gemm<T, false, false, PTL>(y, C, PN, t0, sl, PN, p0, 0, NT);
+    const float ea = sc.e[ta], eb = sc.e[tb];
+#pragma unroll
+    for (int j = 0; j < PTL; ++j) {
+        y[j][0] *= ea, y[j][1] *= ea;
+        y[j][2] *= eb, y[j][3] *= eb;
+    }
+    const float cha = sc.ch[ta], cla = sc.cl[ta], chb = sc.ch[tb], clb = sc.cl[tb];
+#pragma unroll 1
+    for (int s0 = 0; s0 <= t0; s0 += 16) {
+        float m[2][4];
+        zero_acc(m);
+        warp_gemm<T, false, false, 2>(m, C, PN, t0, B, PN, s0, 0, NT);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int s = s0 + 8 * j + 2 * q;
+            const float2 chs = *reinterpret_cast<const float2*>(sc.ch + s);
+            const float2 cls = *reinterpret_cast<const float2*>(sc.cl + s);
+            const float2 ws = *reinterpret_cast<const float2*>(sc.w + s);
+            m[j][0] = s <= ta ? m[j][0] * (ex2((cha - chs.x) + (cla - cls.x)) * ws.x) : 0.f;
+            m[j][1] = s + 1 <= ta ? m[j][1] * (ex2((cha - chs.y) + (cla - cls.y)) * ws.y) : 0.f;
+            m[j][2] = s <= tb ? m[j][2] * (ex2((chb - chs.x) + (clb - cls.x)) * ws.x) : 0.f;
+            m[j][3] = s + 1 <= tb ? m[j][3] * (ex2((chb - chs.y) + (clb - cls.y)) * ws.y) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k += M::KT) {
+            typename M::A fa;
+            M::from_acc(fa, m + k);
+#pragma unroll
+            for (int j = 0; j < PTL; j += 2) {
+                typename M::B b0, b1;
+                M::load_bt2(b0, b1, x, PP, p0 + 8 * j, s0 + 8 * k);
+                if constexpr (FINITE) M::keep_finite(b0), M::keep_finite(b1);
+                M::mma(y[j], fa, b0);
+                M::mma(y[j + 1], fa, b1);
+            }
+        }
+    }
+}
+
+template <typename T, int NT, int MODE>
+__global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>::blocks) heads_walk_kernel(HeadsArgs a, const T* dout) {
+    using W = Walk<T, NT, MODE>;
+    using M = Mma<T>;
+    constexpr int PP = W::PITCH_P, PN = W::PITCH_N, WC = W::WC, kWork = 32 * W::NW;
+    constexpr int NTL = NT / 8 / WC, PTL = kHeadDim / 8 / WC;   // accumulator tiles of a warp
+    constexpr bool kRev = MODE == kWalkLocalRev;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<WalkSmem<T, NT, MODE>*>(smem_raw);
+    auto& sm = *reinterpret_cast<typename W::Smem*>(smem_raw);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int wr = w / WC, wc = w % WC;
     const int64_t b = blockIdx.y, seg = blockIdx.x / a.H;
     const int h = (int)(blockIdx.x - seg * a.H), grp = h / (a.H / a.G);
     const int64_t c0 = seg * a.seg_chunks, c1 = c0 + a.seg_chunks < a.chunks ? c0 + a.seg_chunks : a.chunks;
-    const int64_t bh = b * a.H + h;
-    const T *u = static_cast<const T*>(a.u), *z = static_cast<const T*>(a.z);
-    const T* Bm = static_cast<const T*>(MODE == kWalkLocalRev ? a.C : a.B);
+    const int64_t bh = b * a.H + h, n = c1 - c0;
+    const T *u = static_cast<const T*>(kRev ? (const void*)dout : a.u), *z = static_cast<const T*>(a.z);
+    const T *Bm = static_cast<const T*>(kRev ? a.C : a.B), *Cm = static_cast<const T*>(a.C);
+    auto chunk = [&](int64_t i) { return kRev ? c1 - 1 - i : c0 + i; };
 
-    // the state: rows p = 16 w + g and + 8, columns n = 8 j + 2 q and + 1
+    if (w == W::NW) {
+        // the scalars of chunk i + 1 while the others work on chunk i
+        chunk_scalars<T>(sm.s[0], a, b, h, chunk(0) * kQ);
+        for (int64_t i = 0; i < n; ++i) {
+            __syncthreads();
+            if (i + 1 < n) chunk_scalars<T>(sm.s[(i + 1) & 1], a, b, h, chunk(i + 1) * kQ);
+            if (W::stages == 1) __syncthreads();
+        }
+        return;
+    }
+
+    auto fetch = [&](int64_t i) {
+        const int64_t t0 = chunk(i) * kQ, rows = a.L - t0 < kQ ? a.L - t0 : kQ;
+        const int64_t row = (b * a.L + t0) * a.H + h, rowg = (b * a.L + t0) * a.G + grp;
+        auto& t = sm.t[W::stages == 2 ? i & 1 : 0];
+        load_tile_async<T, kHeadDim>(t.x, PP, u + row * a.P, (int64_t)a.H * a.P, rows, a.P, a.vec, tid, kWork);
+        load_tile_async<T, NT>(t.B, PN, Bm + rowg * a.N, (int64_t)a.G * a.N, rows, a.N, a.vec, tid, kWork);
+        if (W::out) load_tile_async<T, NT>(t.C, PN, Cm + rowg * a.N, (int64_t)a.G * a.N, rows, a.N, a.vec, tid, kWork);
+        if (kRev && z)
+            load_tile_async<T, kHeadDim>(t.zr, PP, z + row * a.P, (int64_t)a.H * a.P, rows, a.P, a.vec, tid, kWork);
+    };
+
+    // the state: rows p = 16 wr + g and + 8, columns n = (NT / WC) wc + 8 j + 2 q and + 1
+    const int p0 = 16 * wr, n0 = NT / WC * wc;
     float S[NTL][4];
     zero_acc(S);
-    const float* first = MODE != kWalkOut ? nullptr
-                         : a.nseg > 1     ? a.states + (bh * a.nseg + seg) * a.P * a.N
-                         : a.h0           ? a.h0 + bh * a.P * a.N
-                                          : nullptr;
     auto each_state = [&](auto&& fn) {
 #pragma unroll
         for (int j = 0; j < NTL; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int p = 16 * w + g + (i >> 1) * 8, n = 8 * j + 2 * q + (i & 1);
-                if (p < a.P && n < a.N) fn(S[j][i], (int64_t)p * a.N + n);
+                const int p = p0 + g + (i >> 1) * 8, m = n0 + 8 * j + 2 * q + (i & 1);
+                if (p < a.P && m < a.N) fn(S[j][i], (int64_t)p * a.N + m);
             }
     };
-    if (first) each_state([&](float& v, int64_t at) { v = first[at]; });
+    if (MODE == kWalkOut) {
+        const float* first = a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N
+                             : a.h0     ? a.h0 + bh * a.P * a.N
+                                        : nullptr;
+        if (first) each_state([&](float& v, int64_t at) { v = first[at]; });
+    }
     double total = 0.0;
+    if (W::stages == 2) {
+        fetch(0);
+        cp_async_commit();
+    }
 
-    for (int64_t ci = 0; ci < c1 - c0; ++ci) {
-        const int64_t c = MODE == kWalkLocalRev ? c1 - 1 - ci : c0 + ci;
-        const int64_t t0 = c * kQ, rows = a.L - t0 < kQ ? a.L - t0 : kQ;
-        const int64_t row = (b * a.L + t0) * a.H + h, rowg = (b * a.L + t0) * a.G + grp;
-        __syncthreads();  // the last chunk's readers are done
-        load_tile<T, kHeadDim>(sm.x, Pt::P, (MODE == kWalkLocalRev ? dout : u) + row * a.P, (int64_t)a.H * a.P, rows,
-                               a.P, a.vec, tid, kThreads);
-        load_tile<T, NT>(sm.B, Pt::N, Bm + rowg * a.N, (int64_t)a.G * a.N, rows, a.N, a.vec, tid, kThreads);
-        if constexpr (MODE == kWalkOut) {
-            load_tile<T, NT>(sm.C, Pt::N, static_cast<const T*>(a.C) + rowg * a.N, (int64_t)a.G * a.N, rows, a.N, a.vec,
-                             tid, kThreads);
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t t0 = chunk(i) * kQ, rows = a.L - t0 < kQ ? a.L - t0 : kQ;
+        const int64_t row = (b * a.L + t0) * a.H + h;
+        auto& t = sm.t[W::stages == 2 ? i & 1 : 0];
+        if (W::stages == 1) {
+            __syncthreads();  // the last chunk's readers are done
+            fetch(i);
+            cp_async_commit();
+        }
+        cp_async_wait<0>();
+        __syncthreads();      // this chunk's tiles and scalars are here; with two buffers, the other one is free
+        const ChunkScalars& sc = sm.s[i & 1];
+        if constexpr (W::out) {
+            if (z)
+                load_tile_async<T, kHeadDim>(sm.z, PP, z + row * a.P, (int64_t)a.H * a.P, rows, a.P, a.vec, tid, kWork);
+            cp_async_commit();
+        }
+        if (W::stages == 2) {
+            if (i + 1 < n) fetch(i + 1);
+            cp_async_commit();
+        }
+
+        if constexpr (W::out) {
+            // the state as the outputs read it, and f B
 #pragma unroll
             for (int j = 0; j < NTL; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    split_store<T>(sm.sh, sm.sl, (16 * w + g + (i >> 1) * 8) * Pt::N + 8 * j + 2 * q + (i & 1), S[j][i]);
-        }
-        if (w == 0) chunk_scalars<T>(sm.s, a, b, h, t0);
-        __syncthreads();
-        // the scaled copy of x; in reverse the scale is exp(c_t) and SiLU(z) comes in too
-        int bad = 0;
-        for (int i = tid; i < kQ * kHeadDim; i += kThreads) {
-            const int t = i / kHeadDim, p = i - t * kHeadDim;
-            float v = to_f32<T>(sm.x[t * Pt::P + p]);
-            if constexpr (MODE == kWalkLocalRev) {
-                if (z && t < rows && p < a.P) v *= silu(to_f32<T>(z[(row + (int64_t)t * a.H) * a.P + p]));
-                split_store<T>(sm.fh, sm.fl, t * Pt::P + p, v * sm.s.e[t]);
-            } else {
-                split_store<T>(sm.fh, sm.fl, t * Pt::P + p, v * sm.s.f[t]);
-                if (MODE == kWalkOut && !(fabsf(v) <= 3.4e38f)) {
-                    // a value that is not finite must not meet the zeros of M above the diagonal:
-                    // it is left out of the product and added to its own rows below
-                    bad = 1;
-                    sm.x[t * Pt::P + p] = from_f32<T>(0.f);
+                for (int k = 0; k < 2; ++k) {
+                    const int at = (p0 + g + 8 * k) * PN + n0 + 8 * j + 2 * q;
+                    const float x = S[j][2 * k], y = S[j][2 * k + 1];
+                    if constexpr (W::bf16) {
+                        const uint32_t hi = M::pack(x, y);
+                        *reinterpret_cast<uint32_t*>(sm.sh + at) = hi;
+                        *reinterpret_cast<uint32_t*>(sm.sl + at) =
+                            M::pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+                    } else {
+                        *reinterpret_cast<float2*>(sm.sh + at) = make_float2(x, y);
+                    }
+                }
+            if constexpr (W::scale_b) {
+#pragma unroll
+                for (int k = tid; k < kQ * NT / 2; k += kWork) {
+                    const int s = k / (NT / 2), at = s * PN + (k - s * (NT / 2)) * 2;
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(t.B + at);
+                    float x = __uint_as_float(v << 16) * sc.f[s], y = __uint_as_float(v & 0xffff0000u) * sc.f[s];
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        const uint32_t r = Mma<__nv_bfloat16>::pack(x, y);
+                        *reinterpret_cast<uint32_t*>(sm.fb[part] + at) = r;
+                        x -= __uint_as_float(r << 16);
+                        y -= __uint_as_float(r & 0xffff0000u);
+                    }
                 }
             }
-        }
-        if (MODE == kWalkOut) bad = __syncthreads_or(bad);
-        else __syncthreads();
+            product_sync<kWork>();
 
-        if constexpr (MODE == kWalkOut) {
             float y[PTL][4];
-            zero_acc(y);
-            warp_gemm<T, false, false, PTL>(y, sm.C, Pt::N, 16 * w, sm.sh, Pt::N, 0, 0, NT);
-            if constexpr (!M::kExact32) warp_gemm<T, false, false, PTL>(y, sm.C, Pt::N, 16 * w, sm.sl, Pt::N, 0, 0, NT);
-            const int ta = 16 * w + g, tb = ta + 8;
+            const int c_p = kHeadDim / WC * wc;
+            const int ta = p0 + g, tb = ta + 8;              // the rows of y are steps
+            const T* sl = W::bf16 ? sm.sl : nullptr;
+            chunk_outputs<T, NT, PTL, false>(y, t.C, t.B, t.x, sm.sh, sl, sc, p0, c_p);
+            // A value of u that is not finite meets the zeros of M above the diagonal in the product.
+            // Where a result is not finite, the product is taken again without such values and the
+            // terms that do hold them are added: they reach no earlier step.
+            float probe = 0.f;
 #pragma unroll
-            for (int j = 0; j < PTL; ++j) {
-                y[j][0] *= sm.s.e[ta];
-                y[j][1] *= sm.s.e[ta];
-                y[j][2] *= sm.s.e[tb];
-                y[j][3] *= sm.s.e[tb];
+            for (int j = 0; j < PTL; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) probe = fmaf(y[j][k], 0.f, probe);
+            if (__any_sync(0xffffffffu, probe != 0.f)) {
+                chunk_outputs<T, NT, PTL, true>(y, t.C, t.B, t.x, sm.sh, sl, sc, p0, c_p);
+#pragma unroll
+                for (int j = 0; j < PTL; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        y[j][k] += not_finite_terms(t.C, t.B, t.x, sc, PN, PP, a.N, k < 2 ? ta : tb,
+                                                    c_p + 8 * j + 2 * q + (k & 1));
             }
-            // M U, 16 columns s of M at a time, up to the diagonal
-            for (int s0 = 0; s0 <= 16 * w; s0 += 16) {
-                float m[2][4];
-                zero_acc(m);
-                warp_gemm<T, false, false, 2>(m, sm.C, Pt::N, 16 * w, sm.B, Pt::N, s0, 0, NT);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = ta + (i >> 1) * 8, s = s0 + 8 * j + 2 * q + (i & 1);
-                        m[j][i] = s <= t ? m[j][i] * (chunk_decay(sm.s, t, s) * sm.s.w[s]) : 0.f;
-                    }
-#pragma unroll
-                for (int k = 0; k < 2; k += M::KT) {
-                    typename M::A fa;
-                    M::from_acc(fa, m + k);
-#pragma unroll
-                    for (int j = 0; j < PTL; j += 2) {
-                        typename M::B b0, b1;
-                        M::load_bt2(b0, b1, sm.x, Pt::P, 8 * j, s0 + 8 * k);
-                        M::mma(y[j], fa, b0);
-                        M::mma(y[j + 1], fa, b1);
-                    }
-                }
-            }
+            // skip term and gate, through the gate's own rows of shared memory to 16-byte stores
+            if (W::stages == 2) cp_async_wait<1>();
+            else cp_async_wait<0>();
+            product_sync<kWork>();
             const float D = a.D ? __ldg(a.D + h) : 0.f;
 #pragma unroll
             for (int j = 0; j < PTL; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const int t = ta + (i >> 1) * 8, p = 8 * j + 2 * q;
-                    if (t >= rows) continue;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (p + k >= a.P) continue;
-                        const int64_t at = (row + (int64_t)t * a.H) * a.P + p + k;
-                        float v = y[j][i + k];
-                        float x = to_f32<T>(sm.x[t * Pt::P + p + k]);
-                        if (bad) {
-                            x = to_f32<T>(u[at]);
-                            for (int s = 0; s <= t; ++s) {
-                                const float xs = to_f32<T>(u[(row + (int64_t)s * a.H) * a.P + p + k]);
-                                if (fabsf(xs) <= 3.4e38f) continue;
-                                float dot = 0.f;
-                                for (int n = 0; n < a.N; ++n)
-                                    dot = fmaf(to_f32<T>(sm.C[t * Pt::N + n]), to_f32<T>(sm.B[s * Pt::N + n]), dot);
-                                v += dot * (chunk_decay(sm.s, t, s) * sm.s.w[s]) * xs;
-                            }
-                        }
-                        v = a.D ? fmaf(D, x, v) : v;
-                        if (z) v *= silu(to_f32<T>(z[at]));
-                        static_cast<T*>(a.out)[at] = from_f32<T>(v);
+                for (int k = 0; k < 2; ++k) {
+                    const int at = (k ? tb : ta) * PP + c_p + 8 * j + 2 * q;
+                    float xv[2], v[2] = {y[j][2 * k], y[j][2 * k + 1]};
+                    load_shared2(t.x + at, xv);
+                    if (a.D) v[0] = fmaf(D, xv[0], v[0]), v[1] = fmaf(D, xv[1], v[1]);
+                    if (z) {
+                        float zv[2];
+                        load_shared2(sm.z + at, zv);
+                        v[0] *= silu(zv[0]), v[1] *= silu(zv[1]);
                     }
+                    store_vec<2>(sm.z + at, v);
                 }
+            __syncwarp();
+            constexpr int VE = 16 / sizeof(T), PER = kHeadDim / WC / VE;
+            T* out = static_cast<T*>(a.out);
+#pragma unroll
+            for (int k = lane; k < 16 * PER; k += 32) {
+                const int r = k / PER, st = p0 + r, p = c_p + (k - r * PER) * VE;
+                if (st >= rows || p >= a.P) continue;
+                const int64_t at = (row + (int64_t)st * a.H) * a.P + p;
+                if (a.vec) {
+                    *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(sm.z + st * PP + p);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VE; ++v)
+                        if (p + v < a.P) out[at + v] = sm.z[st * PP + p + v];
+                }
+            }
         }
+
         // S' = exp(c_end) S + (f U)^T B
-        const float dec = ex2(sm.s.total * kLog2e);
-        total += sm.s.total;
+        const float dec = ex2(sc.total * kLog2e);
+        total += sc.total;
+        float hi[NTL][4], lo[NTL][4];
+        zero_acc(hi);
+        zero_acc(lo);
+        if constexpr (W::scale_b) {
+#pragma unroll
+            for (int k = 0; k < kQ; k += M::KS) {
+                typename M::A fa;
+                M::load_at(fa, t.x, PP, p0, k);
+#pragma unroll
+                for (int part = 2; part >= 0; --part)
+#pragma unroll
+                    for (int j = 0; j < NTL; j += 2) {
+                        typename M::B b0, b1;
+                        M::load_bt2(b0, b1, sm.fb[part], PN, n0 + 8 * j, k);
+                        M::mma(part ? lo[j] : hi[j], fa, b0);
+                        M::mma(part ? lo[j + 1] : hi[j + 1], fa, b1);
+                    }
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < kQ; k += M::KS) {
+                Split<T> fa;
+                load_at_split(fa, t.x, PP, p0, k, [&](float v, int p, int s) {
+                    if (!kRev) return v * sc.f[s];
+                    return (z ? v * silu(to_f32<T>(t.zr[s * PP + p])) : v) * sc.e[s];
+                });
+#pragma unroll
+                for (int j = 0; j < NTL; j += 2) {
+                    typename M::B b0, b1;
+                    M::load_bt2(b0, b1, t.B, PN, n0 + 8 * j, k);
+                    mma_split(hi[j], lo[j], fa, b0);
+                    mma_split(hi[j + 1], lo[j + 1], fa, b1);
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NTL; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[j][i] *= dec;
-        warp_gemm<T, true, true, NTL>(S, sm.fh, Pt::P, 16 * w, sm.B, Pt::N, 0, 0, kQ);
-        if constexpr (!M::kExact32) warp_gemm<T, true, true, NTL>(S, sm.fl, Pt::P, 16 * w, sm.B, Pt::N, 0, 0, kQ);
+            for (int k = 0; k < 4; ++k) S[j][k] = fmaf(dec, S[j][k], hi[j][k] + lo[j][k]);
     }
-    if constexpr (MODE == kWalkOut) {
+    if (MODE == kWalkOut) {
         if (a.h_last && seg == a.nseg - 1) {
             float* o = a.h_last + bh * a.P * a.N;
             each_state([&](float& v, int64_t at) { o[at] = v; });
@@ -281,10 +444,12 @@ __global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* sta
 template <typename T, int NT, int MODE>
 cudaError_t walk(const HeadsArgs& a, const void* dout, cudaStream_t st) {
     auto* k = heads_walk_kernel<T, NT, MODE>;
-    constexpr size_t smem = sizeof(WalkSmem<T, NT, MODE>);
+    using W = Walk<T, NT, MODE>;
+    constexpr size_t smem = sizeof(typename W::Smem);
+    static_assert(smem <= 227 * 1024, "the tiles of one chunk must fit a block's shared memory");
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k<<<dim3((unsigned)(a.H * a.nseg), (unsigned)a.batch), kThreads, smem, st>>>(a, static_cast<const T*>(dout));
+    k<<<dim3((unsigned)(a.H * a.nseg), (unsigned)a.batch), W::threads, smem, st>>>(a, static_cast<const T*>(dout));
     api_count_launch();
     return cudaGetLastError();
 }

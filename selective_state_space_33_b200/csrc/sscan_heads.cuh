@@ -37,8 +37,8 @@ struct HeadsArgs {
     float* decays;            // [batch][H][nseg]: sum of q over the segment
 };
 
-// Scalars of one chunk's steps, and their running sums.
-struct ChunkScalars {
+// Scalars of one chunk's steps, and their running sums (read two at a time, hence the alignment).
+struct alignas(16) ChunkScalars {
     float ch[kQ], cl[kQ];     // log2(e) c_t as the sum of two floats: the difference of two of
                               // them keeps its absolute error near 2^-24 whatever c_t's size
     float w[kQ];
@@ -123,6 +123,22 @@ __device__ __forceinline__ void load_tile(T* dst, int pitch, const T* src, int64
             }
         }
         *reinterpret_cast<uint4*>(dst + r * pitch + c) = v;
+    }
+}
+
+// The same by cp.async where vec allows it; the caller commits and waits.
+template <typename T, int COLS>
+__device__ __forceinline__ void load_tile_async(T* dst, int pitch, const T* src, int64_t stride, int64_t rows, int cols,
+                                                bool vec, int tid, int threads) {
+    if (!vec) {
+        load_tile<T, COLS>(dst, pitch, src, stride, rows, cols, false, tid, threads);
+        return;
+    }
+    constexpr int VE = 16 / sizeof(T), PER = COLS / VE;
+    for (int i = tid; i < kQ * PER; i += threads) {
+        const int r = i / PER, c = (i - r * PER) * VE;
+        const bool in = r < rows && c < cols;
+        cp_async16(dst + r * pitch + c, in ? src + r * stride + c : src, in);
     }
 }
 

@@ -58,6 +58,14 @@ template <> struct Mma<__nv_bfloat16> {
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                      : "=r"(b0.r[0]), "=r"(b0.r[1]), "=r"(b1.r[0]), "=r"(b1.r[1]) : "r"(p) : "memory");
     }
+    // infinities and NaN (all exponent bits set) become 0
+    static __device__ __forceinline__ void keep_finite(B& b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if ((b.r[i] & 0x7f80u) == 0x7f80u) b.r[i] &= 0xffff0000u;
+            if ((b.r[i] & 0x7f800000u) == 0x7f800000u) b.r[i] &= 0xffffu;
+        }
+    }
     static __device__ __forceinline__ uint32_t pack(float x, float y) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
         return *reinterpret_cast<const uint32_t*>(&v);
@@ -127,6 +135,11 @@ template <> struct Mma<float> {
         load_bt(b0, s, pitch, n0, k0);
         load_bt(b1, s, pitch, n0 + 8, k0);
     }
+    static __device__ __forceinline__ void keep_finite(B& b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if ((b.hi[i] & 0x7f800000u) == 0x7f800000u) b.hi[i] = b.lo[i] = 0u;
+    }
     static __device__ __forceinline__ void from_acc(A& a, const float (*c)[4]) {
         put(a, 0, c[0][0]);
         put(a, 1, c[0][2]);
@@ -165,6 +178,77 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[NTL][4], const T* A, int 
             M::mma(acc[j + 1], a, b1);
         }
     }
+}
+
+// An A fragment of products v_i that are not exact in the tile type, as parts whose sum is v to
+// 2^-24: three bf16 fragments, or the one fp32 fragment (itself two tf32 parts).
+template <typename T> struct Split;
+template <> struct Split<__nv_bfloat16> {
+    static constexpr int PARTS = 3;
+    Mma<__nv_bfloat16>::A part[3];
+    __device__ __forceinline__ void set(int i, float x, float y) {  // register i: k and k + 1 of one row
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const uint32_t v = Mma<__nv_bfloat16>::pack(x, y);
+            part[p].r[i] = v;
+            x -= __uint_as_float(v << 16);
+            y -= __uint_as_float(v & 0xffff0000u);
+        }
+    }
+};
+template <> struct Split<float> {
+    static constexpr int PARTS = 1;
+    Mma<float>::A part[1];
+};
+
+// The fragment at rows m0, k0 of a tile stored [k][m], every element passed through
+// fn(value, row m, k) and split.
+template <typename Fn>
+__device__ __forceinline__ void load_at_split(Split<__nv_bfloat16>& a, const __nv_bfloat16* s, int pitch, int m0, int k0,
+                                              Fn fn) {
+    Mma<__nv_bfloat16>::A raw;
+    Mma<__nv_bfloat16>::load_at(raw, s, pitch, m0, k0);
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + g + (i & 1) * 8, k = k0 + 2 * t + (i >> 1) * 8;
+        a.set(i, fn(__uint_as_float(raw.r[i] << 16), m, k), fn(__uint_as_float(raw.r[i] & 0xffff0000u), m, k + 1));
+    }
+}
+template <typename Fn>
+__device__ __forceinline__ void load_at_split(Split<float>& a, const float* s, int pitch, int m0, int k0, Fn fn) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const float* p = s + (k0 + 2 * t) * pitch + m0 + g;
+    Mma<float>::put(a.part[0], 0, fn(p[0], m0 + g, k0 + 2 * t));
+    Mma<float>::put(a.part[0], 1, fn(p[8], m0 + g + 8, k0 + 2 * t));
+    Mma<float>::put(a.part[0], 2, fn(p[pitch], m0 + g, k0 + 2 * t + 1));
+    Mma<float>::put(a.part[0], 3, fn(p[pitch + 8], m0 + g + 8, k0 + 2 * t + 1));
+}
+
+// Products with the leading parts go to `hi`, the corrections to `lo`: the tensor core's
+// accumulation drops low bits at each step, so the small terms are kept apart, the large
+// ones take fewer steps, and the caller adds the two in fp32.
+__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const Split<__nv_bfloat16>& a,
+                                          const Mma<__nv_bfloat16>::B& b) {
+    Mma<__nv_bfloat16>::mma(lo, a.part[2], b);
+    Mma<__nv_bfloat16>::mma(lo, a.part[1], b);
+    Mma<__nv_bfloat16>::mma(hi, a.part[0], b);
+}
+__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const Split<float>& a, const Mma<float>::B& b) {
+    Mma<float>::one(lo, a.part[0].lo, b.hi);
+    Mma<float>::one(lo, a.part[0].hi, b.lo);
+    Mma<float>::one(hi, a.part[0].hi, b.hi);
+}
+
+// 16 bytes from global to shared memory, asynchronously; zeros when !in (src is then not read).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int n = in ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int NTL>

@@ -65,6 +65,14 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[V]) {
     t.get(x);
 }
 
+// Two neighbouring elements of a shared-memory tile.
+template <typename T>
+__device__ __forceinline__ void load_shared2(const T* p, float (&x)[2]) {
+    Vec<T, 2> t;
+    t.load_rw(p);
+    t.get(x);
+}
+
 template <int V, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
     Vec<T, V> t;
