@@ -13,5 +13,6 @@ _BINDING_NAMES = ("sscan_fwd", "sscan_last_state", "sscan_bwd", "sscan_step", "s
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found directly from now on
+        return value
     raise AttributeError(name)

@@ -415,9 +415,9 @@ def _at(t):
 def _on(device, stream, body):
     """body(raw stream) with `device` current and allocations made for the stream that the
     kernels run on, so that a workspace freed on return is not reused before they are done."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream().cuda_stream)
     if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
         with torch.cuda.device(device):
             return body(torch.cuda.current_stream().cuda_stream)
     if stream.device != device:
@@ -426,7 +426,22 @@ def _on(device, stream, body):
         return body(stream.cuda_stream)
 
 
+def _match(t, name, shape, dtype, device):
+    """_expect, with the checks that pass taken first (a one-token call spends its time here)."""
+    if t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+                     and t.is_contiguous()):
+        return
+    _expect(t, name, shape, dtype, device)
+
+
+def _require(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+
+
 def _io_tensor(t, name, ndim, what):
+    if type(t) is torch.Tensor and t.dim() == ndim and t.dtype in _IO_CODES and t.is_cuda and t.is_contiguous():
+        return t.device, t.dtype
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != ndim:
@@ -458,8 +473,8 @@ def _conv_args(u, weight, bias, ndim, silu):
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a (D, K) tensor")
     D, K = u.shape[-1], weight.shape[1]
-    _expect(weight, "weight", (D, K), torch.float32, dev)
-    _expect(bias, "bias", (D,), torch.float32, dev)
+    _match(weight, "weight", (D, K), torch.float32, dev)
+    _match(bias, "bias", (D,), torch.float32, dev)
     L = u.shape[1] if ndim == 3 else 1
     return dev, io, ConvProblem(u.shape[0], L, D, K, _IO_CODES[io], SSCAN_CONV_SILU if silu else 0)
 
@@ -470,8 +485,8 @@ def sscan_conv_fwd(u, weight, bias=None, state0=None, *, silu=True, out=None, re
     or ``(out, state_last)``."""
     dev, io, prob = _conv_args(u, weight, bias, 3, silu)
     window = (prob.batch, max(prob.taps - 1, 0), prob.dim)
-    _expect(state0, "state0", window, io, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(state0, "state0", window, io, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out
@@ -486,9 +501,9 @@ def sscan_conv_bwd(u, weight, dout, bias=None, state0=None, *, silu=True, want_d
     """Gradients of sum(out * dout) of sscan_conv_fwd: a dict keyed du, dweight and, when the
     matching input is given, dbias and dstate0 (unless ``want_dstate0`` is false)."""
     dev, io, prob = _conv_args(u, weight, bias, 3, silu)
-    _expect(state0, "state0", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
+    _match(state0, "state0", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
     _require(dout, "dout")
-    _expect(dout, "dout", u.shape, io, dev)
+    _match(dout, "dout", u.shape, io, dev)
 
     def body(st):
         lib = load_library()
@@ -509,8 +524,8 @@ def sscan_conv_step(u, weight, state, bias=None, *, silu=True, out=None, stream=
     out (batch, D)."""
     dev, io, prob = _conv_args(u, weight, bias, 2, silu)
     _require(state, "state")
-    _expect(state, "state", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(state, "state", (prob.batch, max(prob.taps - 1, 0), prob.dim), io, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out
@@ -519,20 +534,15 @@ def sscan_conv_step(u, weight, state, bias=None, *, silu=True, out=None, stream=
     return _on(dev, stream, body)
 
 
-def _require(t, name):
-    if t is None:
-        raise ValueError(f"{name} is required")
-
-
 def _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, ndim, rate):
     dev, io = _io_tensor(u, "u", ndim, "(batch, L, D)" if ndim == 3 else "(batch, D)")
     for t, name in ((a_raw, "a_raw"), (i_raw, "i_raw"), (Lam, "Lam")):
         _require(t, name)
     D = u.shape[-1]
-    _expect(a_raw, "a_raw", u.shape, io, dev)
-    _expect(i_raw, "i_raw", u.shape, io, dev)
+    _match(a_raw, "a_raw", u.shape, io, dev)
+    _match(i_raw, "i_raw", u.shape, io, dev)
     for t, name in ((Lam, "Lam"), (a_bias, "a_bias"), (i_bias, "i_bias")):
-        _expect(t, name, (D,), torch.float32, dev)
+        _match(t, name, (D,), torch.float32, dev)
     return dev, io, GatedProblem(u.shape[0], u.shape[1] if ndim == 3 else 1, D, _IO_CODES[io], rate)
 
 
@@ -543,8 +553,8 @@ def sscan_gated_fwd(u, a_raw, i_raw, Lam, a_bias=None, i_bias=None, h0=None, *, 
     the biases (D) fp32; h0 (batch, D) fp32.  Returns ``out`` (the h_t), followed by h_last
     (batch, D) and by the checkpoints that sscan_gated_bwd takes, where asked for."""
     dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 3, rate)
-    _expect(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         lib = load_library()
@@ -567,10 +577,10 @@ def sscan_gated_bwd(u, a_raw, i_raw, Lam, dout, a_bias=None, i_bias=None, h0=Non
     ``checkpoints``: what sscan_gated_fwd saved (else a pass over the inputs rebuilds them)."""
     dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 3, rate)
     _require(dout, "dout")
-    _expect(dout, "dout", u.shape, io, dev)
-    _expect(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
+    _match(dout, "dout", u.shape, io, dev)
+    _match(h0, "h0", (prob.batch, prob.dim), torch.float32, dev)
     if checkpoints is not None:
-        _expect(checkpoints, "checkpoints", (prob.batch, load_library().sscan_gated_checkpoints(prob), prob.dim),
+        _match(checkpoints, "checkpoints", (prob.batch, load_library().sscan_gated_checkpoints(prob), prob.dim),
                 torch.float32, dev)
 
     def body(st):
@@ -597,8 +607,8 @@ def sscan_gated_step(u, a_raw, i_raw, Lam, state, a_bias=None, i_bias=None, *, r
     (batch, D), the new state rounded to u's dtype."""
     dev, io, prob = _gated_args(u, a_raw, i_raw, Lam, a_bias, i_bias, 2, rate)
     _require(state, "state")
-    _expect(state, "state", u.shape, torch.float32, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(state, "state", u.shape, torch.float32, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out
@@ -614,14 +624,14 @@ def _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, ndim, delta_softpl
         _require(t, name)
     if not isinstance(B, torch.Tensor) or B.dim() != ndim:
         raise ValueError("B must be (batch, L, groups, N)" if ndim == 4 else "B must be (batch, groups, N)")
-    lead, H, P = tuple(u.shape[:-2]), u.shape[-2], u.shape[-1]
+    lead, H, P = u.shape[:-2], u.shape[-2], u.shape[-1]
     G, N = B.shape[-2], B.shape[-1]
-    _expect(delta_raw, "delta_raw", lead + (H,), io, dev)
-    _expect(z, "z", u.shape, io, dev)
-    _expect(B, "B", lead + (G, N), io, dev)
-    _expect(C, "C", lead + (G, N), io, dev)
+    _match(delta_raw, "delta_raw", lead + (H,), io, dev)
+    _match(z, "z", u.shape, io, dev)
+    _match(B, "B", lead + (G, N), io, dev)
+    _match(C, "C", lead + (G, N), io, dev)
     for t, name in ((A, "A"), (delta_bias, "delta_bias"), (D_skip, "D_skip")):
-        _expect(t, name, (H,), torch.float32, dev)
+        _match(t, name, (H,), torch.float32, dev)
     return dev, io, HeadsProblem(lead[0], lead[1] if ndim == 4 else 1, H, P, N, G, _IO_CODES[io],
                                  SSCAN_DELTA_SOFTPLUS if delta_softplus else 0)
 
@@ -634,8 +644,8 @@ def sscan_heads_fwd(u, delta_raw, A, B, C, delta_bias=None, D_skip=None, z=None,
     (heads) fp32; h0 (batch, heads, P, N) fp32.  Returns ``out`` or ``(out, h_last)``."""
     dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 4, delta_softplus)
     state = (prob.batch, prob.heads, prob.headdim, prob.dstate)
-    _expect(h0, "h0", state, torch.float32, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(h0, "h0", state, torch.float32, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         lib = load_library()
@@ -655,8 +665,8 @@ def sscan_heads_bwd(u, delta_raw, A, B, C, dout, delta_bias=None, D_skip=None, z
     dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 4, delta_softplus)
     state = (prob.batch, prob.heads, prob.headdim, prob.dstate)
     _require(dout, "dout")
-    _expect(dout, "dout", u.shape, io, dev)
-    _expect(h0, "h0", state, torch.float32, dev)
+    _match(dout, "dout", u.shape, io, dev)
+    _match(h0, "h0", state, torch.float32, dev)
 
     def body(st):
         lib = load_library()
@@ -680,8 +690,8 @@ def sscan_heads_step(u, delta_raw, A, B, C, state, delta_bias=None, D_skip=None,
     (batch, heads, P, N) fp32 updated in place.  Returns out (batch, heads, P)."""
     dev, io, prob = _heads_args(u, delta_raw, A, B, C, delta_bias, D_skip, z, 3, delta_softplus)
     _require(state, "state")
-    _expect(state, "state", (prob.batch, prob.heads, prob.headdim, prob.dstate), torch.float32, dev)
-    _expect(out, "out", u.shape, io, dev)
+    _match(state, "state", (prob.batch, prob.heads, prob.headdim, prob.dstate), torch.float32, dev)
+    _match(out, "out", u.shape, io, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out

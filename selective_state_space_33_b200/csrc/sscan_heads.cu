@@ -406,36 +406,73 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
     }
 }
 
-// One token: a warp owns `rows` channels of one (batch, head) in turn; lanes run along n.
-template <typename T>
-__global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* state) {
-    const int lane = threadIdx.x & 31;
+// One token.  It moves 8 N bytes of state per channel and is bound by HBM bandwidth.  LPR lanes
+// share the N states of a channel, four neighbouring ones each (V = 4, one 16-byte access) or one
+// at a time; a warp takes kStepRows channels per lane group of one (batch, head), so that the
+// scalars of that pair, some 80 instructions, are worked out once for 4 kStepRows states.
+constexpr int kStepRows = 4;
+
+template <typename T, int LPR, int V>
+__global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* state, int units) {
+    constexpr int RW = 32 / LPR;  // channels side by side in a warp
+    const int lane = threadIdx.x & 31, r0 = lane / LPR, l = lane % LPR;
     const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t bh = unit / a.P;
+    const int64_t bh = unit / units;
     if (bh >= a.batch * a.H) return;
-    const int p = (int)(unit - bh * a.P);
+    const int p0 = (int)(unit - bh * units) * RW * kStepRows + r0;
     const int64_t b = bh / a.H;
     const int h = (int)(bh - b * a.H);
     const int64_t bg = b * a.G + h / (a.H / a.G);
-    const float A = __ldg(a.A + h);
+    const T *Bp = static_cast<const T*>(a.B) + bg * a.N, *Cp = static_cast<const T*>(a.C) + bg * a.N;
+
+    float x[kStepRows], zv[kStepRows];
+    Vec<float, V> s[kStepRows];
+    const bool one = V * LPR >= a.N;  // every state of a channel is in one access of its lanes
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) {
+        const int p = p0 + k * RW;
+        if (p >= a.P) continue;
+        if (one && l * V < a.N) s[k].load_rw(state + (bh * a.P + p) * a.N + l * V);
+        x[k] = IO<T>::load(static_cast<const T*>(a.u), bh * a.P + p);
+        zv[k] = a.z ? IO<T>::load(static_cast<const T*>(a.z), bh * a.P + p) : 0.f;
+    }
+    const float A = __ldg(a.A + h), D = a.D ? __ldg(a.D + h) : 0.f;
     const float r = IO<T>::load(static_cast<const T*>(a.delta_raw), bh) + (a.bias ? __ldg(a.bias + h) : 0.f);
     const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
-    const float qv = dl * A, dec = ex2(qv * kLog2e);
-    const float x = IO<T>::load(static_cast<const T*>(a.u), bh * a.P + p);
-    const float wx = (A != 0.f ? expm1f(qv) / A : dl) * x;
-    float* sp = state + (bh * a.P + p) * a.N;
-    float y = 0.f;
-    for (int n = lane; n < a.N; n += 32) {
-        const float s = fmaf(dec, sp[n], wx * IO<T>::load(static_cast<const T*>(a.B), bg * a.N + n));
-        sp[n] = s;
-        y = fmaf(s, IO<T>::load(static_cast<const T*>(a.C), bg * a.N + n), y);
+    const float qv = dl * A, dec = ex2(qv * kLog2e), w = A != 0.f ? expm1f(qv) / A : dl;
+    float y[kStepRows];
+#pragma unroll
+    for (int k = 0; k < kStepRows; ++k) y[k] = 0.f;
+    for (int n = l * V; n < a.N; n += LPR * V) {
+        float Bn[V], Cn[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) Bn[v] = IO<T>::load(Bp, n + v), Cn[v] = IO<T>::load(Cp, n + v);
+#pragma unroll
+        for (int k = 0; k < kStepRows; ++k) {
+            const int p = p0 + k * RW;
+            if (p >= a.P) continue;
+            float* sp = state + (bh * a.P + p) * a.N + n;
+            if (!one) s[k].load_rw(sp);
+            float sv[V];
+            s[k].get(sv);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                sv[v] = fmaf(dec, sv[v], w * x[k] * Bn[v]);
+                y[k] = fmaf(sv[v], Cn[v], y[k]);
+            }
+            store_vec<V>(sp, sv);
+        }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (lane == 0) {
-        if (a.D) y = fmaf(__ldg(a.D + h), x, y);
-        if (a.z) y *= silu(IO<T>::load(static_cast<const T*>(a.z), bh * a.P + p));
-        IO<T>::store(static_cast<T*>(a.out), bh * a.P + p, y);
+    for (int k = 0; k < kStepRows; ++k) {
+#pragma unroll
+        for (int o = 1; o < LPR; o *= 2) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
+        const int p = p0 + k * RW;
+        if (l == 0 && p < a.P) {
+            float v = a.D ? fmaf(D, x[k], y[k]) : y[k];
+            if (a.z) v *= silu(zv[k]);
+            IO<T>::store(static_cast<T*>(a.out), bh * a.P + p, v);
+        }
     }
 }
 
@@ -460,6 +497,29 @@ cudaError_t walk_n(const HeadsArgs& a, const void* dout, cudaStream_t st) {
     if (a.N <= 32) return walk<T, 32, MODE>(a, dout, st);
     if (a.N <= 64) return walk<T, 64, MODE>(a, dout, st);
     return walk<T, 128, MODE>(a, dout, st);
+}
+
+template <typename T, int LPR, int V>
+void step_heads(const HeadsArgs& a, float* state, cudaStream_t st) {
+    constexpr int per = 32 / LPR * kStepRows;
+    const int units = (a.P + per - 1) / per;
+    heads_step_kernel<T, LPR, V><<<(unsigned)((a.batch * a.H * units + 3) / 4), 128, 0, st>>>(a, state, units);
+}
+
+// Four states per lane where rows of the state are 16-byte aligned, with as many lanes per
+// channel as that takes (a power of two).
+template <typename T>
+void launch_step_heads(const HeadsArgs& a, float* state, cudaStream_t st) {
+    if (a.N % 4 == 0 && aligned_to(state, 16)) {
+        if (a.N <= 16) step_heads<T, 4, 4>(a, state, st);
+        else if (a.N <= 32) step_heads<T, 8, 4>(a, state, st);
+        else if (a.N <= 64) step_heads<T, 16, 4>(a, state, st);
+        else step_heads<T, 32, 4>(a, state, st);
+    } else if (a.N <= 8) {
+        step_heads<T, 8, 1>(a, state, st);
+    } else {
+        step_heads<T, 32, 1>(a, state, st);
+    }
 }
 
 // Segments of a forward pass: one block per (batch, head) where those fill the GPU, else
@@ -611,9 +671,8 @@ sscan_status sscan_heads_step(const sscan_heads_problem* p, const void* u, const
         return api_fail(SSCAN_ERR_UNSUPPORTED, "more than 2^32 (batch, head, channel) rows");
     HeadsArgs a = heads_args(p, u, delta_raw, delta_bias, A, B, C, D_skip, z, nullptr);
     a.out = out;
-    const unsigned blocks = (unsigned)((a.batch * a.H * a.P + 3) / 4);
-    if (p->io_dtype == SSCAN_BF16) heads_step_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(a, state);
-    else heads_step_kernel<float><<<blocks, 128, 0, st>>>(a, state);
+    if (p->io_dtype == SSCAN_BF16) launch_step_heads<__nv_bfloat16>(a, state, st);
+    else launch_step_heads<float>(a, state, st);
     api_count_launch();
     return api_launched("heads step kernel");
 }
