@@ -5,9 +5,9 @@
 //
 // Every element is read and written once, against K multiply-adds and (with SiLU) two
 // special-function operations, so all three are bound by HBM bandwidth.  A thread owns V
-// neighbouring channels (V elements in one 16-byte access where width and pointers allow
-// it, else 2 or 1) and walks a stretch of steps with the window in registers; loads of
-// kAhead rows are issued before any of them is used.
+// neighbouring channels (4 or 2 elements in one access where width and pointers allow it) and
+// walks a stretch of steps with the window in registers; the loads of several rows are issued
+// before any of them is used.
 #include <cuda_runtime.h>
 
 #include <initializer_list>
@@ -29,6 +29,7 @@ struct ConvArgs {
     void* out;            // (batch, L, D)
     void* last;           // (batch, K-1, D) or null
     int64_t tile;         // steps per thread, a multiple of kAhead
+    int wide_w;           // weight on a 16-byte boundary
     // backward
     const void* dout;     // (batch, L, D)
     void* du;             // (batch, L, D)
@@ -52,12 +53,19 @@ __device__ __forceinline__ void load_row(const ConvArgs& a, int64_t b, int64_t t
     }
 }
 
+// Rows of the weight come in one access each where they are aligned to their size.
 template <int K, int V>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t d, float (&w)[K][V], float (&bias)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        const float* p = a.w + (d + v) * K;
+        if (K == 4 && a.wide_w) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p));
+            w[0][v] = f.x, w[1][v] = f.y, w[K - 2][v] = f.z, w[K - 1][v] = f.w;
+        } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][v] = __ldg(a.w + (d + v) * K + k);
+            for (int k = 0; k < K; ++k) w[k][v] = __ldg(p + k);
+        }
         bias[v] = a.bias ? __ldg(a.bias + d + v) : 0.f;
     }
 }
@@ -65,13 +73,14 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t d, float (&
 // One thread: V channels of one batch row, `tile` steps.  Threads run along the channels
 // first, so that a warp's accesses are consecutive.
 template <typename T, int K, int V, bool kSilu>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(128, 8) conv_fwd_kernel(ConvArgs a) {
     const int64_t cols = a.D / V;
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t row = i / cols;
     if (row >= a.batch * a.tiles) return;
     const int64_t d = (i - row * cols) * V, b = row / a.tiles, t0 = (row - b * a.tiles) * a.tile;
-    const int64_t t1 = t0 + a.tile < a.L ? t0 + a.tile : a.L;
+    const int64_t left = a.L - t0;
+    int n = (int)(left < a.tile ? left : a.tile);
 
     float w[K][V], bias[V], x[K - 1][V];
     load_taps<K, V>(a, d, w, bias);
@@ -79,32 +88,44 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(ConvArgs a) {
     for (int k = 0; k < K - 1; ++k) load_row<T, K, V>(a, b, t0 - (K - 1) + k, d, x[k]);
     const T* up = static_cast<const T*>(a.u) + (b * a.L + t0) * a.D + d;
     T* op = static_cast<T*>(a.out) + (b * a.L + t0) * a.D + d;
-    for (int64_t t = t0; t < t1; t += kAhead) {
-        Vec<T, V> in[kAhead];
+    auto step = [&](const Vec<T, V>& in) {
+        float xn[V], y[V];
+        in.get(xn);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (t + j < t1) in[j].load(up + j * a.D);
+        for (int v = 0; v < V; ++v) {
+            float s = fmaf(w[K - 1][v], xn[v], bias[v]);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (t + j >= t1) break;
-            float xn[V], y[V];
-            in[j].get(xn);
+            for (int k = 0; k < K - 1; ++k) s = fmaf(w[k][v], x[k][v], s);
+            y[v] = kSilu ? silu(s) : s;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float s = fmaf(w[K - 1][v], xn[v], bias[v]);
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) s = fmaf(w[k][v], x[k][v], s);
-                y[v] = kSilu ? silu(s) : s;
-#pragma unroll
-                for (int k = 0; k < K - 2; ++k) x[k][v] = x[k + 1][v];
-                x[K - 2][v] = xn[v];
-            }
-            store_vec<V>(op + j * a.D, y);
+            for (int k = 0; k < K - 2; ++k) x[k][v] = x[k + 1][v];
+            x[K - 2][v] = xn[v];
         }
-        up += kAhead * a.D;
-        op += kAhead * a.D;
+        store_vec<V>(op, y);
+        op += a.D;
+    };
+    constexpr int N = V * sizeof(T) > 8 ? kAhead / 2 : kAhead;  // at most 64 bytes of loads ahead
+#pragma unroll 1
+    for (; n >= N; n -= N) {
+        Vec<T, V> in[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            in[j].load(up);
+            up += a.D;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) step(in[j]);
     }
-    if (a.last && t1 == a.L) {
+    if (n > 0) {
+        Vec<T, V> in[N];
+#pragma unroll
+        for (int j = 0; j < N - 1; ++j)
+            if (j < n) in[j].load(up + j * a.D);
+#pragma unroll
+        for (int j = 0; j < N - 1; ++j)
+            if (j < n) step(in[j]);
+    }
+    if (a.last && t0 + a.tile >= a.L) {
         // the window now holds the last K - 1 inputs; each was read exactly, so this is a copy
 #pragma unroll
         for (int k = 0; k < K - 1; ++k)
@@ -119,7 +140,7 @@ constexpr int kBwdGroups = 8;  // stretches per block, whose dW partials the blo
 // K-1 steps past its stretch to have every dy its dx needs (recomputed, not exchanged: two
 // rows in `tile`), and the block writes one row of dW and dbias partial sums.
 template <typename T, int K, int V, bool kSilu>
-__global__ void __launch_bounds__(32 * kBwdGroups) conv_bwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a) {
     __shared__ float red[kBwdGroups][(K + 1) * V][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t d = ((int64_t)blockIdx.x * 32 + lane) * V;
@@ -144,62 +165,75 @@ __global__ void __launch_bounds__(32 * kBwdGroups) conv_bwd_kernel(ConvArgs a) {
         for (int v = 0; v < V; ++v) x[0][v] = 0.f;
         const T* up = static_cast<const T*>(a.u) + (b * a.L + t0) * a.D + d;
         const T* gp = static_cast<const T*>(a.dout) + (b * a.L + t0) * a.D + d;
-        constexpr int kStep = kAhead / 2;
-        for (int64_t s = t0; s < t1 + K - 1; s += kStep) {
-            Vec<T, V> in[kStep], gin[kStep];
+        T* dp = static_cast<T*>(a.du) + (b * a.L + t0) * a.D + d;
+        const int own = (int)(t1 - t0);                      // steps of this stretch
+        const int have = (int)(a.L - t0 < own + K - 1 ? a.L - t0 : own + K - 1);  // and those there are past it
+        // step s of the stretch: dy_s, its share of dW, and dx of K - 1 steps earlier
+        auto step = [&](int s, const Vec<T, V>& in, const Vec<T, V>& gin) {
+            float xn[V], gv[V], dx[V];
+            in.get(xn);
+            gin.get(gv);
 #pragma unroll
-            for (int j = 0; j < kStep; ++j)
-                if (s + j < t1 + K - 1 && s + j < a.L) {
-                    in[j].load(up + j * a.D);
-                    gin[j].load(gp + j * a.D);
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int k = 0; k < K - 1; ++k) {
+                    x[k][v] = x[k + 1][v];
+                    dy[k][v] = dy[k + 1][v];
                 }
+                x[K - 1][v] = xn[v];
+                float dyt = gv[v];
+                if (kSilu) {
+                    float y = bias[v];
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) {
-                const int64_t t = s + j;
-                if (t >= t1 + K - 1) break;
-                float xn[V], g[V], dx[V];
-                if (t < a.L) {
-                    in[j].get(xn);
-                    gin[j].get(g);
+                    for (int k = 0; k < K; ++k) y = fmaf(w[k][v], x[k][v], y);
+                    dyt *= dsilu(y);
                 }
+                if (s >= have) dyt = 0.f;                    // past the sequence
+                dy[K - 1][v] = dyt;
+                if (s < own) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-#pragma unroll
-                    for (int k = 0; k < K - 1; ++k) {
-                        x[k][v] = x[k + 1][v];
-                        dy[k][v] = dy[k + 1][v];
-                    }
-                    dy[K - 1][v] = 0.f;
-                    if (t < a.L) {
-                        x[K - 1][v] = xn[v];
-                        float dyt = g[v];
-                        if (kSilu) {
-                            float y = bias[v];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) y = fmaf(w[k][v], x[k][v], y);
-                            dyt *= dsilu(y);
-                        }
-                        dy[K - 1][v] = dyt;
-                        if (t < t1) {
-#pragma unroll
-                            for (int k = 0; k < K; ++k) sums[k][v] = fmaf(dyt, x[k][v], sums[k][v]);
-                            sums[K][v] += dyt;
-                        }
-                    }
-                    // dy[j] is dy_{t-K+1+j}; dx_{t-K+1} = sum_k W[k] dy_{t-k}
-                    dx[v] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) dx[v] = fmaf(w[k][v], dy[K - 1 - k][v], dx[v]);
+                    for (int k = 0; k < K; ++k) sums[k][v] = fmaf(dyt, x[k][v], sums[k][v]);
+                    sums[K][v] += dyt;
                 }
-                const int64_t tx = t - (K - 1);
-                if (tx >= t0) {
-                    store_vec<V>(static_cast<T*>(a.du) + (b * a.L + tx) * a.D + d, dx);
-                } else if (tx < 0 && a.dstate0) {  // only the first stretch gets here with tx < 0
-                    store_vec<V>(static_cast<T*>(a.dstate0) + (b * (K - 1) + t) * a.D + d, dx);
-                }
+                // dy[j] is dy_{s-K+1+j}; dx_{s-K+1} = sum_k W[k] dy_{s-k}
+                dx[v] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) dx[v] = fmaf(w[k][v], dy[K - 1 - k][v], dx[v]);
             }
-            up += kStep * a.D;
-            gp += kStep * a.D;
+            if (s >= K - 1) {
+                store_vec<V>(dp, dx);
+                dp += a.D;
+            } else if (t0 == 0 && a.dstate0) {
+                store_vec<V>(static_cast<T*>(a.dstate0) + (b * (K - 1) + s) * a.D + d, dx);
+            }
+        };
+        constexpr int N = 4;
+        int s = 0;
+#pragma unroll 1
+        for (; s + N <= have; s += N) {
+            Vec<T, V> in[N], gin[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                in[j].load(up);
+                gin[j].load(gp);
+                up += a.D;
+                gp += a.D;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) step(s + j, in[j], gin[j]);
+        }
+#pragma unroll 1
+        for (; s < own + K - 1; ++s) {
+            Vec<T, V> in, gin;
+            in.zero();
+            gin.zero();
+            if (s < have) {
+                in.load(up);
+                gin.load(gp);
+                up += a.D;
+                gp += a.D;
+            }
+            step(s, in, gin);
         }
     }
 #pragma unroll
@@ -271,7 +305,7 @@ enum { kConvFwd, kConvBwd, kConvStep };
 
 template <typename T, int K, int V, bool kSilu>
 void launch_one(int op, const ConvArgs& a, cudaStream_t st) {
-    if (op == kConvBwd) {
+    if constexpr (V <= 2) if (op == kConvBwd) {
         const dim3 grid((unsigned)((a.D / V + 31) / 32), (unsigned)(a.batch * a.tiles));
         conv_bwd_kernel<T, K, V, kSilu><<<grid, 32 * kBwdGroups, 0, st>>>(a);
         return;
@@ -279,7 +313,7 @@ void launch_one(int op, const ConvArgs& a, cudaStream_t st) {
     const int64_t n = (op == kConvFwd ? a.batch * a.tiles : a.batch) * (a.D / V);
     const unsigned blocks = (unsigned)((n + 127) / 128);
     if (op == kConvFwd) conv_fwd_kernel<T, K, V, kSilu><<<blocks, 128, 0, st>>>(a);
-    else conv_step_kernel<T, K, V, kSilu><<<blocks, 128, 0, st>>>(a);
+    else if constexpr (V <= 2) conv_step_kernel<T, K, V, kSilu><<<blocks, 128, 0, st>>>(a);
 }
 
 template <typename T, int K, int V>
@@ -295,11 +329,11 @@ void launch_taps(int op, const ConvArgs& a, int taps, bool act, cudaStream_t st)
     else launch_silu<T, 4, V>(op, a, act, st);
 }
 
-// The widest access that the width and every pointer allow.  (The backward keeps 3 K + 2
-// fp32 values per channel in registers, so there a thread owns at most 4 channels.)
+// The widest access that the width and every pointer allow, up to 4 channels in the forward
+// pass and 2 elsewhere: the backward keeps 3 K + 2 fp32 values per channel in registers, and a
+// step has so few elements that it wants more threads rather than wider ones.
 int conv_width(int op, int64_t D, size_t es, std::initializer_list<const void*> ptrs) {
-    for (int v : {16 / (int)es, 2}) {
-        if (op == kConvBwd && v > 4) v = 4;
+    for (int v = op == kConvFwd ? 4 : 2; v > 1; v /= 2) {
         bool ok = D % v == 0;
         for (const void* p : ptrs) ok = ok && aligned_to(p, v * es);
         if (ok) return v;
@@ -307,18 +341,18 @@ int conv_width(int op, int64_t D, size_t es, std::initializer_list<const void*> 
     return 1;
 }
 
-void launch_conv(int op, const ConvArgs& a, int taps, bool act, bool bf16, cudaStream_t st) {
+template <typename T>
+void launch_width(int op, const ConvArgs& a, int v, int taps, bool act, cudaStream_t st) {
+    if (v == 4) launch_taps<T, 4>(op, a, taps, act, st);
+    else if (v == 2) launch_taps<T, 2>(op, a, taps, act, st);
+    else launch_taps<T, 1>(op, a, taps, act, st);
+}
+
+void launch_conv(int op, ConvArgs a, int taps, bool act, bool bf16, cudaStream_t st) {
+    a.wide_w = aligned_to(a.w, 16);
     const int v = conv_width(op, a.D, bf16 ? 2 : 4, {a.u, a.state0, a.out, a.last, a.dout, a.du, a.dstate0});
-    if (bf16) {
-        if (v == 8) launch_taps<__nv_bfloat16, 8>(op, a, taps, act, st);
-        else if (v == 4) launch_taps<__nv_bfloat16, 4>(op, a, taps, act, st);
-        else if (v == 2) launch_taps<__nv_bfloat16, 2>(op, a, taps, act, st);
-        else launch_taps<__nv_bfloat16, 1>(op, a, taps, act, st);
-    } else {
-        if (v == 4) launch_taps<float, 4>(op, a, taps, act, st);
-        else if (v == 2) launch_taps<float, 2>(op, a, taps, act, st);
-        else launch_taps<float, 1>(op, a, taps, act, st);
-    }
+    if (bf16) launch_width<__nv_bfloat16>(op, a, v, taps, act, st);
+    else launch_width<float>(op, a, v, taps, act, st);
     api_count_launch();
 }
 
@@ -338,11 +372,12 @@ sscan_status check_conv(const sscan_conv_problem* p) {
     return api_elements(p->batch, p->seqlen, p->dim);
 }
 
-// Steps per thread: 32 keeps the K-1 rows that a stretch re-reads below a tenth of its own;
-// few threads (under two blocks of 128 per SM) take 8, which is one batch of loads.
+// Steps per thread, a multiple of kAhead from 8 to 48: what makes one wave of threads (8 blocks of
+// 128 per SM), so that small problems spread out and large ones re-read few rows (K-1 per
+// stretch).  8 x 2048 x 1536 bf16: 25.2 us at the 48 this gives, 26.5, 28.0 and 27.4 at 24, 32, 64.
 int64_t conv_fwd_tile(const sscan_conv_problem* p) {
-    const int64_t threads = p->batch * ((p->seqlen + 31) / 32) * (p->dim / (p->io_dtype == SSCAN_BF16 ? 8 : 4));
-    return threads >= 148 * 256 ? 32 : kAhead;
+    const int64_t n = (p->batch * p->seqlen * ((p->dim + 3) / 4) / (148 * 1024) + kAhead - 1) / kAhead * kAhead;
+    return n < kAhead ? kAhead : n > 48 ? 48 : n;
 }
 
 // The backward's stretch: 32 steps; blocks (of kBwdGroups stretches) along one sequence are

@@ -23,6 +23,7 @@ struct Vec {
     __device__ __forceinline__ void load(const T* p) { r = __ldg(reinterpret_cast<const R*>(p)); }
     // memory that this thread itself overwrites later
     __device__ __forceinline__ void load_rw(const T* p) { r = *reinterpret_cast<const R*>(p); }
+    __device__ __forceinline__ void zero() { r = R{}; }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<R*>(p) = r; }
     __device__ __forceinline__ void get(float (&x)[V]) const {
         if constexpr (sizeof(T) == 4) {
