@@ -3,28 +3,43 @@
 //   a = exp(-s),  m = sqrt(1 - a^2),   h_t = a_t h_{t-1} + m_t i_t u_t,   out_t = h_t,
 // for every (batch, channel); its backward pass and its one-token step.
 //
-// One pass over the sequence.  A block owns a tile of kTile steps by 32 V channels: each of
-// its kWarps warps scans kSteps consecutive steps from zero with the gates' results in
-// registers, the warps' affine maps h -> A h + H are combined through shared memory, the
-// state entering the tile comes from the tiles before it, and a second sweep over the
-// registers writes the outputs.  So every input is read once and every output written once,
-// however the sequence is split.
+// One pass over the sequence.  A block owns a tile of kWarps x S steps by 32 V channels (S = 16
+// forward, 8 backward): each of its kWarps working warps scans S consecutive steps from zero
+// with the gates' results in registers, the warps' affine maps h -> A h + H are combined through
+// shared memory, the state entering the tile comes from the tiles before it, and a second sweep
+// over the registers writes the outputs.  So every input is read once and every output written
+// once, however the sequence is split.
 //
-// The carry between tiles (chain_carry): tiles take their place in line from an atomic
-// ticket in time order, so all tiles a block waits for have already started.  A tile
-// publishes its own map as soon as it has it; the state entering a group of kGroup tiles is
-// handed on by the last tile of the group before.  A tile composes the maps of its group's
-// earlier tiles, in order, and applies them to the group's state: the grouping is fixed, so
-// two runs round alike, and the serial chain has one hop per kGroup * kTile steps.
+// A fixed number of blocks take tile after tile.  While a tile is computed, the next one's inputs
+// are on their way to shared memory.  Results overwrite the inputs they came from there.  Rows and widths on 16-byte boundaries travel by
+// TMA, which also fills and clips the edges; others by the working warps.
+//
+// The carry between tiles: tickets run in time order, so whatever a tile waits for is held by a
+// block that has started and waits only for earlier tiles.  One extra warp of a block (carry_in)
+// waits for the earlier tiles' maps while the others compute; another (carry_out) publishes this
+// tile's map as soon as it is known.  Tiles are composed in a fixed tree: the maps of kFan tiles
+// make a group's, published by its last tile, and the state entering kFan groups is handed on by
+// their last tile.  So two runs round alike, a tile reads at most 2 (kFan - 1) maps and one state,
+// all at once, and the serial chain has one hop per kFan^2 tiles.  A published word is its own
+// flag: the arrays start as all ones, a NaN that no arithmetic returns, and each 8-byte word is
+// stored and polled whole, so no fence or second round trip is needed.
+//
+// Per element the forward moves 4 I/O elements against 4 special-function operations (5 where a
+// channel's decay can pass exp(-1/4)) and some 24 issued instructions; two elements, V = 2
+// channels or two steps, share each packed fp32 instruction.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstddef>
+#include <type_traits>
 
 #include "sscan_check.cuh"
 #include "sscan_host.h"
 #include "sscan_launch.h"
 #include "sscan_math.cuh"
 #include "sscan_rowsum.cuh"
+#include "sscan_tma.cuh"
 #include "sscan_vec.cuh"
 
 namespace sscan {
@@ -34,18 +49,20 @@ __device__ unsigned int g_device_error_gated = 0;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kSteps = 8;                // steps per warp
-constexpr int kTile = kWarps * kSteps;   // steps per block; also the checkpoint interval
-constexpr int kGroup = 32;               // tiles per hop of the serial chain
-constexpr uint32_t kPollLimit = 1u << 22;
+constexpr int kStepsFwd = 16, kStepsBwd = 8; // steps per warp
+constexpr int kCkpt = kWarps * kStepsBwd;    // checkpoint interval: a tile of the backward
+constexpr int kFan = 8;                      // tiles per group, groups per hop of the serial chain
+constexpr int kThreads = 32 * (kWarps + 2);  // the working warps, carry_in's and carry_out's
+constexpr uint32_t kPollLimit = 1u << 20;
+constexpr unsigned long long kUnset = ~0ull;
 
+// Every array starts as all ones.
 struct Chain {
-    unsigned int* ticket;   // null: one tile per sequence, no carry
-    unsigned int* mapped;   // [cols][tiles] 1 once the tile's map is published
-    unsigned int* entered;  // [cols][groups] 1 once the group's entering state is published
-    float2* maps;           // [cols][tiles][32 V] (A, H)
-    float* states;          // [cols][groups][32 V]
-    int64_t tiles, groups, cols;
+    unsigned int* ticket;         // null: one tile per sequence, no carry
+    unsigned long long* maps;     // [cols][tiles][32 V] (A, H) of a tile
+    unsigned long long* groups;   // [cols][ngroups][32 V] (A, H) of kFan tiles
+    unsigned long long* states;   // [cols][nsupers][32 V] (h, 0): the state entering kFan groups
+    int64_t tiles, ngroups, nsupers, cols;
 };
 
 struct GatedArgs {
@@ -55,7 +72,7 @@ struct GatedArgs {
     float rate;
     void* out;       // (batch, L, D) or null (checkpoints only)
     float* h_last;   // (batch, D) or null
-    float* ckpt;     // (batch, tiles, D) or null: the state entering each tile
+    float* ckpt;     // (batch, ceil(L / kCkpt), D) or null: the state before every kCkpt-th step
     Chain chain;
     // backward
     const void* dout;
@@ -67,26 +84,17 @@ struct GatedArgs {
     float* state;    // (batch, D)
 };
 
-// expm1(-s) for 0 <= s < 1/4: Taylor series to s^6, the dropped s^7/5040 below 1.3e-8 relative.
-__device__ __forceinline__ float expm1_neg(float s) {
-    const float p = fmaf(s, fmaf(s, fmaf(s, fmaf(s, fmaf(s, 1.f / 720.f, -1.f / 120.f), 1.f / 24.f), -1.f / 6.f), 0.5f), -1.f);
-    return s * p;
-}
-
-// a = exp(-s) and 1 - a^2 = -e (2 + e), e = expm1(-s).  Near s = 0 both come from the series:
-// the difference 1 - a would cancel, and a long memory multiplies a's error by its length.
-__device__ __forceinline__ void decay(float s, float& a, float& om) {
-    const float ea = ex2(-s * kLog2e);
-    const float e = s < 0.25f ? expm1_neg(s) : ea - 1.f;
-    a = 1.f + e;
-    om = -e * (2.f + e);
-}
-
-__device__ __forceinline__ float sqrt_fast(float x) {
+// min(x, 60) that keeps a NaN
+__device__ __forceinline__ float min_nan(float x) {
     float y;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(60.f));
     return y;
 }
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 __device__ __forceinline__ float rsqrt_fast(float x) {
     float y;
@@ -94,196 +102,439 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
     return y;
 }
 
+// 1 / sqrt(om), and a large finite value where om has underflowed to 0 (its products with om and
+// with s are then 0)
+__device__ __forceinline__ float2 rsqrt2(float2 om) {
+    const float2 x = add2(om, splat(1e-36f));
+    return make_float2(rsqrt_fast(x.x), rsqrt_fast(x.y));
+}
+
+// a = exp(-s) and om = 1 - a^2 = e (2 - e), with e = 1 - a.  For s < 1/4, e comes from its Taylor
+// series to s^6 (the dropped s^7/5040 is below 1.3e-8 relative): the difference 1 - a would
+// cancel, and a long memory multiplies a's error by its length.  kAny: s may be 1/4 or more.
+template <bool kAny>
+__device__ __forceinline__ void decay2(float2 s, float2& a, float2& om) {
+    float2 p = fma2(s, splat(-1.f / 720.f), splat(1.f / 120.f));
+    p = fma2(s, p, splat(-1.f / 24.f));
+    p = fma2(s, p, splat(1.f / 6.f));
+    p = fma2(s, p, splat(-0.5f));
+    p = fma2(s, p, splat(1.f));
+    float2 e = mul2(s, p);
+    if (kAny) {
+        if (!(s.x < 0.25f)) e.x = 1.f - ex2(-s.x * kLog2e);
+        if (!(s.y < 0.25f)) e.y = 1.f - ex2(-s.y * kLog2e);
+    }
+    a = fma2(e, splat(-1.f), splat(1.f));
+    om = mul2(e, fma2(e, splat(-1.f), splat(2.f)));
+}
+
+// sigmoid(x + bias) of both gates for two elements, from one reciprocal each:
+// with D = 1 + e^-x,  1 / D_r = D_i / (D_r D_i).  nbias = -log2(e) bias.  Exponents are held to 2^60,
+// so a gate never falls below 2^-60 and the product of the two stays finite.
+__device__ __forceinline__ void gates2(float2 xr, float2 xi, float2 nbr, float2 nbi, float2& r, float2& i) {
+    const float2 qr = fma2(xr, splat(-kLog2e), nbr), qi = fma2(xi, splat(-kLog2e), nbi);
+    const float2 er = make_float2(ex2(min_nan(qr.x)), ex2(min_nan(qr.y)));
+    const float2 ei = make_float2(ex2(min_nan(qi.x)), ex2(min_nan(qi.y)));
+    const float2 dr = add2(er, splat(1.f)), di = add2(ei, splat(1.f)), p = mul2(dr, di);
+    const float2 rp = make_float2(rcp(p.x), rcp(p.y));
+    r = mul2(di, rp);
+    i = mul2(dr, rp);
+}
+
 // rate * softplus(Lam), once per channel of a block
 __device__ __forceinline__ float decay_rate(float lam, float rate) {
     return rate * (lam > 20.f ? lam : log1pf(expf(lam)));
 }
 
-__device__ __forceinline__ unsigned int load_acquire(const unsigned int* p) {
-    unsigned int v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+// A published word, read and written whole past the L1.
+__device__ __forceinline__ unsigned long long poll_word(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
-
-__device__ __forceinline__ void store_release(unsigned int* p, unsigned int v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void put_word(unsigned long long* p, float a, float h) {
+    const unsigned long long v = ((unsigned long long)__float_as_uint(h) << 32) | __float_as_uint(a);
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
-__device__ __forceinline__ bool wait_set(const unsigned int* p) {
-    for (uint32_t i = 0; i < kPollLimit; ++i) {
-        if (load_acquire(p)) return true;
-        __nanosleep(32);
-    }
-    return false;
-}
-
-// One warp: the state entering tile k (in chain order) of column block `col`, for the V
-// channels of each lane, from the tile's own map (A, H) and the state `first` entering tile 0.
-// A wait that gives up raises `err` and goes on, publishing as if it had not, so that no
-// later tile waits for it in turn.
+// Composes the n <= kFan - 1 maps of V channels per lane that start at words + first, each `V * 32`
+// words after the one before, onto (A, H); false when one did not come in time.
 template <int V>
-__device__ __forceinline__ void chain_carry(const Chain& c, int64_t col, int64_t k, const float (&A)[V],
-                                            const float (&H)[V], const float (&first)[V], float (&state)[V],
-                                            unsigned int err) {
-    const int lane = threadIdx.x & 31;
-    const int64_t g = k / kGroup, k0 = g * kGroup;
-    const int n = (int)(k - k0);
-    const bool more = k + 1 < c.tiles, closes = n == kGroup - 1;
-    const int64_t nmaps = c.cols * c.tiles * 32 * V, nstates = c.cols * c.groups * 32 * V;
-    if (more && !closes) {
-        const int64_t at = ((col * c.tiles + k) * 32 + lane) * V;
+__device__ __forceinline__ bool take_maps(const unsigned long long* words, int64_t first, int64_t extent, int n,
+                                          float (&A)[V], float (&H)[V]) {
+    // a map that is not asked for is the identity (1, 0)
+    unsigned long long m[kFan - 1][V];
+    const unsigned long long* p = words + first;
+    bool ready = false;
+#pragma unroll 1
+    for (uint32_t tries = 0; tries < kPollLimit && !ready; ++tries) {
+        ready = true;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (in_range(at + v, nmaps)) __stcg(c.maps + at + v, make_float2(A[v], H[v]));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(c.mapped + col * c.tiles + k, 1u);
+        for (int i = 0; i < kFan - 1; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                m[i][v] = i < n && in_range(first + i * 32 * V + v, extent) ? poll_word(p + i * 32 * V + v) : 0x3f800000ull;
+#pragma unroll
+        for (int i = 0; i < kFan - 1; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) ready = ready && m[i][v] != kUnset;
     }
-    float Ac[V], Hc[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) Ac[v] = 1.f, Hc[v] = 0.f, state[v] = first[v];
-    bool ok = true;
-    if (n > 0) {
-        if (lane < n) ok = wait_set(c.mapped + col * c.tiles + k0 + lane);
-        __syncwarp();
-        __threadfence();
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const int64_t at = ((col * c.tiles + k0 + i) * 32 + lane) * V;
+    for (int i = 0; i < kFan - 1; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 m = in_range(at + v, nmaps) ? __ldcg(c.maps + at + v) : make_float2(0.f, 0.f);
-                Ac[v] *= m.x;
-                Hc[v] = fmaf(m.x, Hc[v], m.y);
+        for (int v = 0; v < V; ++v) {
+            const float a = __uint_as_float((unsigned int)m[i][v]), h = __uint_as_float((unsigned int)(m[i][v] >> 32));
+            H[v] = fmaf(a, H[v], h);
+            A[v] *= a;
+        }
+    return ready;
+}
+
+// What a block knows of the tile it works on.
+struct TileId {
+    unsigned int k;      // rank in chain order
+    unsigned int col, b, blk;
+};
+
+struct ChainSmem {
+    TileId tile[4];          // by iteration
+    float rate[2][64];       // rate softplus(Lam) of the tile's channels, by iteration
+    float in[64];            // the state entering the tile
+    float2 group[64];        // composed maps of the group's earlier tiles
+};
+
+// Barriers of a block besides 0: 1 the tile's maps are in shared memory (working warps and
+// carry_out's), 2 the entering state is (all warps), 3 the group's earlier tiles are composed
+// (the two carry warps), 4 the working warps alone.
+__device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 1, %0;" ::"n"(32 * (kWarps + 1)) : "memory"); }
+__device__ __forceinline__ void sync_state() { asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void sync_work() { asm volatile("bar.sync 4, %0;" ::"n"(32 * kWarps) : "memory"); }
+__device__ __forceinline__ void sync_group() { asm volatile("bar.sync 3, 64;" ::: "memory"); }
+
+__device__ __forceinline__ bool closes_group(unsigned int k) { return k % kFan == kFan - 1; }
+__device__ __forceinline__ bool closes_super(unsigned int k) { return k % (kFan * kFan) == kFan * kFan - 1; }
+
+// carry_in's warp: the state entering tile t of the chain, into s.in; `first` enters tile 0.  A
+// wait that gives up raises `err` and goes on with what it has, and so do the tiles after it.
+template <int V>
+__device__ __forceinline__ void carry_in(const Chain& c, const TileId& t, const float (&first)[V], float (&state)[V],
+                                         ChainSmem& s, unsigned int err) {
+    const int lane = threadIdx.x & 31;
+    const int64_t k = t.k, g = k / kFan, sp = g / kFan, W = 32 * V;
+    float A[V], H[V], Ag[V], Hg[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = Ag[v] = 1.f, H[v] = Hg[v] = 0.f, state[v] = first[v];
+    const int64_t lv = lane * V;
+    bool ok = take_maps<V>(c.maps, (t.col * c.tiles + g * kFan) * W + lv, c.cols * c.tiles * W, (int)(k - g * kFan), A, H);
+    if (closes_group(t.k)) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.group[lv + v] = make_float2(A[v], H[v]);
+        sync_group();
+    }
+    ok = take_maps<V>(c.groups, (t.col * c.ngroups + sp * kFan) * W + lv, c.cols * c.ngroups * W, (int)(g - sp * kFan), Ag, Hg) && ok;
+    if (sp > 0) {
+        const int64_t at = (t.col * c.nsupers + sp) * W + lv;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            unsigned long long m = kUnset;
+            for (uint32_t tries = 0; tries < kPollLimit && m == kUnset; ++tries) {
+                if (tries) __nanosleep(32);
+                m = in_range(at + v, c.cols * c.nsupers * W) ? poll_word(c.states + at + v) : 0ull;
             }
+            ok = ok && m != kUnset;
+            state[v] = __uint_as_float((unsigned int)m);
         }
     }
-    if (g > 0) {
-        if (lane == 0) ok = wait_set(c.entered + col * c.groups + g) && ok;
-        __syncwarp();
-        __threadfence();
-        const int64_t at = ((col * c.groups + g) * 32 + lane) * V;
 #pragma unroll
-        for (int v = 0; v < V; ++v) state[v] = in_range(at + v, nstates) ? __ldcg(c.states + at + v) : 0.f;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) state[v] = fmaf(Ac[v], state[v], Hc[v]);
-    if (more && closes) {
-        const int64_t at = ((col * c.groups + g + 1) * 32 + lane) * V;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (in_range(at + v, nstates)) __stcg(c.states + at + v, fmaf(A[v], state[v], H[v]));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) store_release(c.entered + col * c.groups + g + 1, 1u);
+    for (int v = 0; v < V; ++v) {
+        state[v] = fmaf(A[v], fmaf(Ag[v], state[v], Hg[v]), H[v]);
+        s.in[lv + v] = state[v];
     }
     if (!ok) atomicOr(&g_device_error_gated, err);
 }
 
-// This block's place in line: tickets run through the column blocks first, then the tiles.
-__device__ __forceinline__ void take_ticket(const Chain& c, int64_t& col, int64_t& k) {
-    __shared__ unsigned int place;
-    if (threadIdx.x == 0) place = c.ticket ? atomicAdd(c.ticket, 1u) : blockIdx.x;
-    __syncthreads();
-    k = place / c.cols;
-    col = place - k * c.cols;
+// carry_out's warp, once the tile's own map (A, H) is known: publishes it, or the group's.
+template <int V>
+__device__ __forceinline__ void publish_map(const Chain& c, const TileId& t, const float (&A)[V], const float (&H)[V],
+                                            const ChainSmem& s) {
+    const int lane = threadIdx.x & 31;
+    const int64_t W = 32 * V, lv = lane * V, k = t.k, g = k / kFan;
+    if (closes_group(t.k)) {
+        sync_group();
+        if (k + 1 >= c.tiles || closes_super(t.k)) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 m = s.group[lv + v];
+            const int64_t at = (t.col * c.ngroups + g) * W + lv + v;
+            if (in_range(at, c.cols * c.ngroups * W)) put_word(c.groups + at, A[v] * m.x, fmaf(A[v], m.y, H[v]));
+        }
+    } else if (k + 1 < c.tiles) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t at = (t.col * c.tiles + k) * W + lv + v;
+            if (in_range(at, c.cols * c.tiles * W)) put_word(c.maps + at, A[v], H[v]);
+        }
+    }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(GatedArgs g) {
-    __shared__ float sA[kWarps][32 * V], sH[kWarps][32 * V], sIn[32 * V], sRate[32 * V];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int64_t col, j;
-    take_ticket(g.chain, col, j);
-    const int64_t b = col / g.nblk, d = ((col - b * g.nblk) * 32 + lane) * V;
-    const bool live = d < g.D;  // V divides D, so a lane's channels are all inside or all outside
-    const int64_t t0 = j * kTile + w * kSteps;
-
-    Vec<T, V> u[kSteps], ar[kSteps], ir[kSteps];
-    const int64_t base = (b * g.L + t0) * g.D + d;
+// And once the entering state is: the state after the tile, for the next kFan groups.
+template <int V>
+__device__ __forceinline__ void publish_state(const Chain& c, const TileId& t, const float (&after)[V]) {
+    const int64_t W = 32 * V, lv = (threadIdx.x & 31) * V, k = t.k, at = (t.col * c.nsupers + k / (kFan * kFan) + 1) * W + lv;
+    if (!closes_super(t.k) || k + 1 >= c.tiles) return;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-        if (live && t0 + k < g.L) {
-            ar[k].load(static_cast<const T*>(g.a_raw) + base + k * g.D);
-            ir[k].load(static_cast<const T*>(g.i_raw) + base + k * g.D);
-            u[k].load(static_cast<const T*>(g.u) + base + k * g.D);
-        }
-    if (w < V) {  // channel x of the block, x = 0 .. 32 V - 1
-        const int64_t x = (col - b * g.nblk) * 32 * V + threadIdx.x;
-        sRate[threadIdx.x] = x < g.D ? decay_rate(__ldg(g.Lam + x), g.rate) : 0.f;
-    }
-    float ab[V], ib[V], first[V];
+    for (int v = 0; v < V; ++v)
+        if (in_range(at + v, c.cols * c.nsupers * W)) put_word(c.states + at + v, after[v], 0.f);
+}
+
+// The next ticket of this block, as a tile (k >= tiles: none left).  One thread.
+__device__ __forceinline__ TileId draw_tile(const GatedArgs& g, unsigned int iteration) {
+    const unsigned int place = g.chain.ticket ? atomicAdd(g.chain.ticket, 1u) + 1u : blockIdx.x + iteration * gridDim.x;
+    const unsigned int cols = (unsigned int)g.chain.cols, k = place / cols, col = place - k * cols;
+    const unsigned int nblk = (unsigned int)g.nblk, b = col / nblk;
+    return TileId{k, col, b, col - b * nblk};
+}
+
+// Rates of a tile's 32 V channels (one warp).
+template <int V>
+__device__ __forceinline__ void fill_rates(const GatedArgs& g, const TileId& t, float* rates) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        ab[v] = live && g.a_bias ? __ldg(g.a_bias + d + v) : 0.f;
-        ib[v] = live && g.i_bias ? __ldg(g.i_bias + d + v) : 0.f;
-        first[v] = live && g.h0 && w == 0 ? __ldg(g.h0 + b * g.D + d + v) : 0.f;
+        const int64_t x = (int64_t)t.blk * 32 * V + v * 32 + lane;
+        rates[v * 32 + lane] = x < g.D ? decay_rate(__ldg(g.Lam + x), g.rate) : 0.f;
     }
-    __syncthreads();
-    float a[kSteps][V], x[kSteps][V], A[V], H[V];
+}
+
+// ROWS rows of 32 V elements of a (batch, L, D) tensor from (b, t0, d0) into shared memory, zeros
+// outside, by the working warps.
+template <typename T, int V, int ROWS>
+__device__ __forceinline__ void fetch_rows(T* dst, const void* src, const GatedArgs& g, int64_t b, int64_t t0, int64_t d0) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const bool live = d0 + lane * V < g.D;
+    const T* from = static_cast<const T*>(src) + (b * g.L + t0 + w) * g.D + d0 + lane * V;
+#pragma unroll 8
+    for (int r = w; r < ROWS; r += kWarps, from += kWarps * g.D) {
+        Vec<T, V> v;
+        v.zero();
+        if (live && t0 + r < g.L) v.load(from);
+        v.store(dst + (r * 32 + lane) * V);
+    }
+}
+
+template <typename T, int V, int TENSORS, int STEPS>
+struct GatedSmem {
+    static constexpr int ROWS = kWarps * STEPS, TILE = ROWS * 32 * V, BYTES = TILE * (int)sizeof(T);
+    alignas(128) T rows[2][TENSORS][TILE];  // by iteration
+    uint64_t full[2];
+    float2 AH[kWarps][32 * V];              // maps of the warps; then of all the warps before each
+    ChainSmem c;
+};
+
+// Element pair k (V = 2: step k; V = 1: steps k and k + 1) of a thread's column of a tile.
+template <typename T, int V>
+__device__ __forceinline__ float2 pair_of(const T* rows, int k) {
+    float x[V];
+    load_shared<V>(rows + k * 32 * V, x);
+    if constexpr (V == 2) {
+        return make_float2(x[0], x[1]);
+    } else {
+        float y[V];
+        load_shared<V>(rows + (k + 1) * 32 * V, y);
+        return make_float2(x[0], y[0]);
+    }
+}
+
+// Keeps the compiler from moving shared-memory loads across: left to itself it gathers those of
+// all steps at the start and spills what is already computed (about 1 KB per thread).
+__device__ __forceinline__ void hold_loads() { asm volatile("" ::: "memory"); }
+
+// The gates and the recurrence's terms for the STEPS x V elements of a thread's column of a tile,
+// two at a time: the V = 2 channels of a step, or two steps of the one channel.
+template <typename T, int V, int STEPS, bool kAny, typename Out>
+__device__ __forceinline__ void gate_terms(float2 c, float2 na, float2 ni, const T* ar, const T* ir, const T* u, Out out) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        float uv[V], av[V], iv[V];
-        u[k].get(uv);
-        ar[k].get(av);
-        ir[k].get(iv);
-        const bool in = live && t0 + k < g.L;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float om;
-            decay(sRate[lane * V + v] * sigmoid(av[v] + ab[v]), a[k][v], om);
-            x[k][v] = sqrt_fast(om) * sigmoid(iv[v] + ib[v]) * uv[v];
-            if (!in) a[k][v] = 1.f, x[k][v] = 0.f;  // past the end: the identity map
-            H[v] = fmaf(a[k][v], H[v], x[k][v]);
-            A[v] *= a[k][v];
+    for (int k = 0; k < STEPS; k += 3 - V) {
+        if (k % 4 == 0) hold_loads();
+        float2 r, i, a, om;
+        gates2(pair_of<T, V>(ar, k), pair_of<T, V>(ir, k), na, ni, r, i);
+        decay2<kAny>(mul2(c, r), a, om);
+        const float2 m = mul2(om, rsqrt2(om));
+        out(k, a, mul2(mul2(m, i), pair_of<T, V>(u, k)), r, i);
+    }
+}
+
+template <int V, int STEPS>
+__device__ __forceinline__ void set_pair(float (&v)[STEPS][V], int k, float2 x) {
+    v[k][0] = x.x;
+    if constexpr (V == 2) v[k][1] = x.y;
+    else v[k + 1][0] = x.y;
+}
+
+// Starts a tile's inputs on their way to buffer `buf`: one thread, by TMA.
+template <int TENSORS, typename Smem>
+__device__ __forceinline__ void tma_fetch(Smem& sm, int buf, int first, int n, const CUtensorMap* const (&maps)[TENSORS],
+                                          const TileId& t, int row, int width) {
+    const uint32_t bar = smem_u32(&sm.full[buf]);
+    if (first == 0) mbar_expect_tx(bar, TENSORS * Smem::BYTES);
+    for (int i = first; i < first + n; ++i)
+        tma_load_3d(smem_u32(sm.rows[buf][i]), maps[i], (int)t.blk * width, row, (int)t.b, bar);
+}
+
+template <typename T, int V, bool kTma>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+    gated_fwd_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_i,
+                     const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_out, GatedArgs g) {
+    constexpr int S = kStepsFwd;
+    using Smem = GatedSmem<T, V, 3, S>;
+    constexpr int ROWS = Smem::ROWS;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<Smem*>(smem_raw);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, lv = lane * V;
+    const unsigned int tiles = (unsigned int)g.chain.tiles;
+    const CUtensorMap* const maps[3] = {&tm_a, &tm_i, &tm_u};
+    if (threadIdx.x == 0) {
+        sm.c.tile[0] = draw_tile(g, 0);
+        if (kTma) {
+            mbar_init(smem_u32(&sm.full[0]), 1);
+            mbar_init(smem_u32(&sm.full[1]), 1);
+            fence_proxy_async();
         }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) sA[w][lane * V + v] = A[v], sH[w][lane * V + v] = H[v];
     __syncthreads();
-    if (w == 0) {
-        float state[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) {
-                H[v] = fmaf(sA[q][lane * V + v], H[v], sH[q][lane * V + v]);
-                A[v] *= sA[q][lane * V + v];
+    if (w == kWarps + 1 && sm.c.tile[0].k < tiles) {
+        if (kTma && lane == 0) tma_fetch<3>(sm, 0, 0, 3, maps, sm.c.tile[0], (int)sm.c.tile[0].k * ROWS, 32 * V);
+        fill_rates<V>(g, sm.c.tile[0], sm.c.rate[0]);
+    }
+
+    for (unsigned int it = 0;; ++it) {
+        __syncthreads();  // this tile's place and rates are here, and the last tile is done with
+        const TileId t = sm.c.tile[it & 3];
+        const int buf = it & 1;
+        if (w == kWarps + 1 && lane == 0) {
+            // the last tile's outputs leave, then the next tile's inputs may take their place
+            const TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            sm.c.tile[(it + 1) & 3] = next;
+            const bool more = kTma && next.k < tiles;
+            if (kTma && it > 0 && g.out) {
+                const TileId p = sm.c.tile[(it - 1) & 3];
+                tma_store_3d(&tm_out, (int)p.blk * 32 * V, (int)p.k * ROWS, (int)p.b, smem_u32(sm.rows[buf ^ 1][2]));
             }
+            if (more) tma_fetch<3>(sm, buf ^ 1, 0, 2, maps, next, (int)next.k * ROWS, 32 * V);
+            if (kTma) tma_store_wait_read_0();
+            if (more) tma_fetch<3>(sm, buf ^ 1, 2, 1, maps, next, (int)next.k * ROWS, 32 * V);
         }
-        if (g.chain.ticket) {
-            chain_carry<V>(g.chain, col, j, A, H, first, state, 1u);
-        } else {
+        if (t.k >= tiles) break;
+        const int64_t b = t.b, d = (int64_t)t.blk * 32 * V + lv;
+        const bool live = d < g.D;  // V divides D, so a lane's channels are all inside or all outside
+        if (w == kWarps) {
+            float first[V], state[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) state[v] = first[v];
+            for (int v = 0; v < V; ++v) first[v] = live && g.h0 ? __ldg(g.h0 + b * g.D + d + v) : 0.f;
+            carry_in<V>(g.chain, t, first, state, sm.c, 1u);
+            sync_state();
+            continue;
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) sIn[lane * V + v] = state[v];
-        if (live) {
+        if (w == kWarps + 1) {
+            __syncwarp();
+            if (sm.c.tile[(it + 1) & 3].k < tiles) fill_rates<V>(g, sm.c.tile[(it + 1) & 3], sm.c.rate[buf ^ 1]);
+            sync_maps();
+            float A[V], H[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (g.ckpt) g.ckpt[(b * g.chain.tiles + j) * g.D + d + v] = state[v];
-                if (g.h_last && j == g.chain.tiles - 1) g.h_last[b * g.D + d + v] = fmaf(A[v], state[v], H[v]);
+                A[v] = 1.f, H[v] = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q) {
+                    const float2 m = sm.AH[q][lv + v];
+                    sm.AH[q][lv + v] = make_float2(A[v], H[v]);
+                    H[v] = fmaf(m.x, H[v], m.y);
+                    A[v] *= m.x;
+                }
             }
+            publish_map<V>(g.chain, t, A, H, sm.c);
+            sync_state();
+#pragma unroll
+            for (int v = 0; v < V; ++v) H[v] = fmaf(A[v], sm.c.in[lv + v], H[v]);
+            publish_state<V>(g.chain, t, H);
+            if (live && g.h_last && t.k == tiles - 1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) g.h_last[b * g.D + d + v] = H[v];
+            }
+            continue;
         }
-    }
-    if (!g.out) return;
-    __syncthreads();
-    float h[V];
+
+        const int64_t t0 = (int64_t)t.k * ROWS + w * S;
+        const int own = w * S * 32 * V + lv;
+        T *ar = sm.rows[buf][0] + own, *ir = sm.rows[buf][1] + own, *u = sm.rows[buf][2] + own;
+        if (kTma) {
+            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) atomicOr(&g_device_error_gated, 1u);
+        } else {
+            const int64_t r0 = (int64_t)t.k * ROWS, d0 = (int64_t)t.blk * 32 * V;
+            fetch_rows<T, V, ROWS>(sm.rows[buf][0], g.a_raw, g, b, r0, d0);
+            fetch_rows<T, V, ROWS>(sm.rows[buf][1], g.i_raw, g, b, r0, d0);
+            fetch_rows<T, V, ROWS>(sm.rows[buf][2], g.u, g, b, r0, d0);
+            sync_work();
+        }
+        float nab[V], nib[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        h[v] = sIn[lane * V + v];
-        for (int q = 0; q < w; ++q) h[v] = fmaf(sA[q][lane * V + v], h[v], sH[q][lane * V + v]);
-    }
+        for (int v = 0; v < V; ++v) {
+            nab[v] = live && g.a_bias ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+        }
+        const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
+        const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
+        float a[S][V], x[S][V];
+        auto out = [&](int k, float2 pa, float2 px, float2, float2) {
+            set_pair<V, S>(a, k, pa);
+            set_pair<V, S>(x, k, px);
+        };
+        // r <= 1, so a rate below 1/4 keeps every s of the warp there
+        if (__any_sync(0xffffffffu, !(c.x < 0.25f && c.y < 0.25f))) gate_terms<T, V, S, true>(c, na, ni, ar, ir, u, out);
+        else gate_terms<T, V, S, false>(c, na, ni, ar, ir, u, out);
+        if (t0 + S > g.L) {  // past the end: the identity map
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
+            for (int k = 0; k < S; ++k)
+                if (t0 + k >= g.L) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[k][v], h[v], x[k][v]);
-        if (live && t0 + k < g.L) store_vec<V>(static_cast<T*>(g.out) + base + k * g.D, h);
+                    for (int v = 0; v < V; ++v) a[k][v] = 1.f, x[k][v] = 0.f;
+                }
+        }
+        float A[V], H[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < S; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                H[v] = fmaf(a[k][v], H[v], x[k][v]);
+                A[v] *= a[k][v];
+            }
+#pragma unroll
+        for (int v = 0; v < V; ++v) sm.AH[w][lv + v] = make_float2(A[v], H[v]);
+        sync_maps();
+        sync_state();
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 m = sm.AH[w][lv + v];
+            h[v] = fmaf(m.x, sm.c.in[lv + v], m.y);
+        }
+        if (g.ckpt && t0 % kCkpt == 0 && t0 < g.L && live) {
+            const int64_t rows = (g.L + kCkpt - 1) / kCkpt;
+#pragma unroll
+            for (int v = 0; v < V; ++v) g.ckpt[(b * rows + t0 / kCkpt) * g.D + d + v] = h[v];
+        }
+        if (!g.out) continue;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = fmaf(a[k][v], h[v], x[k][v]);
+            if (kTma) store_vec<V>(u + k * 32 * V, h);
+            else if (live && t0 + k < g.L) store_vec<V>(static_cast<T*>(g.out) + (b * g.L + t0 + k) * g.D + d, h);
+        }
+        if (kTma) fence_proxy_async();
     }
+    if (kTma && w == kWarps + 1 && lane == 0) tma_store_wait_all();
 }
 
 // The adjoint e_t that step t hands to h_{t-1} is affine in the one it gets: with
@@ -293,161 +544,237 @@ __global__ void __launch_bounds__(32 * kWarps) gated_fwd_kernel(GatedArgs g) {
 //   ds = -e_t (h_{t-1} - (a / m) i u),   da_raw = ds s (1 - r),   dLam = sum ds r * rate sigmoid(Lam)
 // Where s underflows to 0, m = 0 and its slope's limit is not finite; that term is left out.
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kWarps, 2) gated_bwd_kernel(GatedArgs g) {
-    __shared__ float sA[kWarps][32 * V], sH[kWarps][32 * V], sE[kWarps][32 * V], sIn[32 * V], sRate[32 * V];
-    __shared__ float red[3][kWarps][32 * V];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int64_t col, rank;
-    take_ticket(g.chain, col, rank);
-    const int64_t j = g.chain.tiles - 1 - rank;
-    const int64_t b = col / g.nblk, d = ((col - b * g.nblk) * 32 + lane) * V;
-    const bool live = d < g.D;
-    const int64_t t0 = j * kTile + w * kSteps;
+struct GatedBwdSmem : GatedSmem<T, V, 4, kStepsBwd> {
+    float2 AE[kWarps][32 * V];              // maps of the adjoint, as AH holds those of the state
+    float red[3][kWarps][32 * V];
+};
 
-    Vec<T, V> u[kSteps], ar[kSteps], ir[kSteps], go[kSteps];
-    const int64_t base = (b * g.L + t0) * g.D + d;
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-        if (live && t0 + k < g.L) {
-            ar[k].load(static_cast<const T*>(g.a_raw) + base + k * g.D);
-            go[k].load(static_cast<const T*>(g.dout) + base + k * g.D);
-            ir[k].load(static_cast<const T*>(g.i_raw) + base + k * g.D);
-            u[k].load(static_cast<const T*>(g.u) + base + k * g.D);
-        }
-    if (w < V) {
-        const int64_t x = (col - b * g.nblk) * 32 * V + threadIdx.x;
-        sRate[threadIdx.x] = x < g.D ? decay_rate(__ldg(g.Lam + x), g.rate) : 0.f;
-    }
-    float ab[V], ib[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        ab[v] = live && g.a_bias ? __ldg(g.a_bias + d + v) : 0.f;
-        ib[v] = live && g.i_bias ? __ldg(g.i_bias + d + v) : 0.f;
-        h[v] = live ? __ldg(g.ckpt_in + (b * g.chain.tiles + j) * g.D + d + v) : 0.f;
-    }
-    __syncthreads();
-    float a[kSteps][V], x[kSteps][V], r[kSteps][V], i[kSteps][V], A[V], H[V], E[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, E[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        float uv[V], av[V], iv[V];
-        u[k].get(uv);
-        ar[k].get(av);
-        ir[k].get(iv);
-        const bool in = live && t0 + k < g.L;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float om;
-            r[k][v] = sigmoid(av[v] + ab[v]);
-            i[k][v] = sigmoid(iv[v] + ib[v]);
-            decay(sRate[lane * V + v] * r[k][v], a[k][v], om);
-            x[k][v] = sqrt_fast(om) * i[k][v] * uv[v];
-            if (!in) a[k][v] = 1.f, x[k][v] = 0.f;
-            H[v] = fmaf(a[k][v], H[v], x[k][v]);
-            A[v] *= a[k][v];
+template <typename T, int V, bool kTma>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+    gated_bwd_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_i,
+                     const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_g,
+                     const __grid_constant__ CUtensorMap tm_da, const __grid_constant__ CUtensorMap tm_di,
+                     const __grid_constant__ CUtensorMap tm_du, GatedArgs g) {
+    constexpr int S = kStepsBwd;
+    using Smem = GatedBwdSmem<T, V>;
+    constexpr int ROWS = Smem::ROWS;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<Smem*>(smem_raw);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, lv = lane * V;
+    const unsigned int tiles = (unsigned int)g.chain.tiles;
+    const CUtensorMap* const maps[4] = {&tm_g, &tm_a, &tm_i, &tm_u};
+    auto row_of = [&](const TileId& t) { return (int)(tiles - 1 - t.k) * ROWS; };
+    if (threadIdx.x == 0) {
+        sm.c.tile[0] = draw_tile(g, 0);
+        if (kTma) {
+            mbar_init(smem_u32(&sm.full[0]), 1);
+            mbar_init(smem_u32(&sm.full[1]), 1);
+            fence_proxy_async();
         }
     }
-#pragma unroll
-    for (int k = kSteps - 1; k >= 0; --k) {
-        float gv[V];
-        go[k].get(gv);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (live && t0 + k < g.L) E[v] = a[k][v] * (gv[v] + E[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sA[w][lane * V + v] = A[v];
-        sH[w][lane * V + v] = H[v];
-        sE[w][lane * V + v] = E[v];
-    }
     __syncthreads();
-    if (w == 0) {
-        float state[V], zero[V];
+    if (w == kWarps + 1 && sm.c.tile[0].k < tiles) {
+        if (kTma && lane == 0) tma_fetch<4>(sm, 0, 0, 4, maps, sm.c.tile[0], row_of(sm.c.tile[0]), 32 * V);
+        fill_rates<V>(g, sm.c.tile[0], sm.c.rate[0]);
+    }
+
+    for (unsigned int it = 0;; ++it) {
+        __syncthreads();  // this tile's place and rates are here, and the last tile is done with but for its sums
+        const TileId t = sm.c.tile[it & 3];
+        const int buf = it & 1;
+        if (w == kWarps + 1 && lane == 0) {
+            const TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            sm.c.tile[(it + 1) & 3] = next;
+            const bool more = kTma && next.k < tiles;
+            if (kTma && it > 0) {
+                const TileId p = sm.c.tile[(it - 1) & 3];
+                const int x = (int)p.blk * 32 * V, y = row_of(p);
+                tma_store_3d_nocommit(&tm_da, x, y, (int)p.b, smem_u32(sm.rows[buf ^ 1][1]));
+                tma_store_3d_nocommit(&tm_di, x, y, (int)p.b, smem_u32(sm.rows[buf ^ 1][2]));
+                tma_store_3d_nocommit(&tm_du, x, y, (int)p.b, smem_u32(sm.rows[buf ^ 1][3]));
+                tma_commit();
+            }
+            if (more) tma_fetch<4>(sm, buf ^ 1, 0, 1, maps, next, row_of(next), 32 * V);
+            if (kTma) tma_store_wait_read_0();
+            if (more) tma_fetch<4>(sm, buf ^ 1, 1, 3, maps, next, row_of(next), 32 * V);
+        }
+        if (it > 0 && w < 3) {
+            // the last tile's sums over its warps
+            const TileId p = sm.c.tile[(it - 1) & 3];
+            const int64_t d = (int64_t)p.blk * 32 * V + lv, j = tiles - 1 - p.k;
+            if (d < g.D) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = 1.f, E[v] = 0.f, zero[v] = 0.f;
+                for (int v = 0; v < V; ++v) {
+                    float s = 0.f;
 #pragma unroll
-            for (int q = kWarps - 1; q >= 0; --q) {
-                E[v] = fmaf(sA[q][lane * V + v], E[v], sE[q][lane * V + v]);
-                A[v] *= sA[q][lane * V + v];
+                    for (int q = 0; q < kWarps; ++q) s += sm.red[w][q][lv + v];
+                    g.part[(((int64_t)p.b * g.chain.tiles + j) * 3 + w) * g.D + d + v] = s;
+                }
             }
         }
-        if (g.chain.ticket) {
-            chain_carry<V>(g.chain, col, rank, A, E, zero, state, 2u);
+        if (t.k >= tiles) break;
+        const int64_t b = t.b, j = tiles - 1 - t.k, d = (int64_t)t.blk * 32 * V + lv;
+        const bool live = d < g.D;
+        if (w == kWarps) {
+            float zero[V], state[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) zero[v] = 0.f;
+            carry_in<V>(g.chain, t, zero, state, sm.c, 2u);
+            sync_state();
+            continue;
+        }
+        if (w == kWarps + 1) {
+            __syncwarp();
+            if (sm.c.tile[(it + 1) & 3].k < tiles) fill_rates<V>(g, sm.c.tile[(it + 1) & 3], sm.c.rate[buf ^ 1]);
+            sync_maps();
+            float A[V], E[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                A[v] = 1.f, E[v] = 0.f;
+#pragma unroll
+                for (int q = kWarps - 1; q >= 0; --q) {
+                    const float2 m = sm.AE[q][lv + v];
+                    sm.AE[q][lv + v] = make_float2(A[v], E[v]);
+                    E[v] = fmaf(m.x, E[v], m.y);
+                    A[v] *= m.x;
+                }
+            }
+            publish_map<V>(g.chain, t, A, E, sm.c);
+            sync_state();
+#pragma unroll
+            for (int v = 0; v < V; ++v) E[v] = fmaf(A[v], sm.c.in[lv + v], E[v]);
+            publish_state<V>(g.chain, t, E);
+            if (live && g.dh0 && j == 0) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) g.dh0[b * g.D + d + v] = E[v];
+            }
+            continue;
+        }
+
+        const int64_t t0 = j * ROWS + w * S;
+        const int own = w * S * 32 * V + lv;
+        T *go = sm.rows[buf][0] + own, *ar = sm.rows[buf][1] + own, *ir = sm.rows[buf][2] + own, *u = sm.rows[buf][3] + own;
+        float nab[V], nib[V], h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nab[v] = live && g.a_bias ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+            h[v] = live ? __ldg(g.ckpt_in + (b * g.chain.tiles + j) * g.D + d + v) : 0.f;
+        }
+        if (kTma) {
+            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) atomicOr(&g_device_error_gated, 2u);
         } else {
+            const int64_t r0 = j * ROWS, d0 = (int64_t)t.blk * 32 * V;
+            fetch_rows<T, V, ROWS>(sm.rows[buf][0], g.dout, g, b, r0, d0);
+            fetch_rows<T, V, ROWS>(sm.rows[buf][1], g.a_raw, g, b, r0, d0);
+            fetch_rows<T, V, ROWS>(sm.rows[buf][2], g.i_raw, g, b, r0, d0);
+            fetch_rows<T, V, ROWS>(sm.rows[buf][3], g.u, g, b, r0, d0);
+            sync_work();
+        }
+        const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
+        const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
+        float a[S][V], x[S][V], r[S][V], i[S][V];
+        auto out = [&](int k, float2 pa, float2 px, float2 pr, float2 pi) {
+            set_pair<V, S>(a, k, pa);
+            set_pair<V, S>(x, k, px);
+            set_pair<V, S>(r, k, pr);
+            set_pair<V, S>(i, k, pi);
+        };
+        const bool any = __any_sync(0xffffffffu, !(c.x < 0.25f && c.y < 0.25f));
+        if (any) gate_terms<T, V, S, true>(c, na, ni, ar, ir, u, out);
+        else gate_terms<T, V, S, false>(c, na, ni, ar, ir, u, out);
+        // past the end dout is zero and so is every adjoint: those steps' terms are zeros by themselves
+        float A[V], H[V], E[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) state[v] = 0.f;
+        for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, E[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < S; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                H[v] = fmaf(a[k][v], H[v], x[k][v]);
+                A[v] *= a[k][v];
+            }
+#pragma unroll
+        for (int k = S - 1; k >= 0; --k) {
+            float gv[V];
+            load_shared<V>(go + k * 32 * V, gv);
+#pragma unroll
+            for (int v = 0; v < V; ++v) E[v] = a[k][v] * (gv[v] + E[v]);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            sIn[lane * V + v] = state[v];
-            if (live && g.dh0 && j == 0) g.dh0[b * g.D + d + v] = fmaf(A[v], state[v], E[v]);
+            sm.AH[w][lv + v] = make_float2(A[v], H[v]);
+            sm.AE[w][lv + v] = make_float2(A[v], E[v]);
         }
-    }
-    // meanwhile the other warps rebuild the states: x[k] becomes h_{t-1}
+        sync_maps();
+        // while the adjoint is on its way: x[k] becomes the state h_{t-1}
+        for (int q = 0; q < w; ++q) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        for (int q = 0; q < w; ++q) h[v] = fmaf(sA[q][lane * V + v], h[v], sH[q][lane * V + v]);
+            for (int v = 0; v < V; ++v) {
+                const float2 m = sm.AH[q][lv + v];
+                h[v] = fmaf(m.x, h[v], m.y);
+            }
+        }
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < S; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float hn = fmaf(a[k][v], h[v], x[k][v]);
+                x[k][v] = h[v];
+                h[v] = hn;
+            }
+        sync_state();
+        // V = 1 computes its one element twice in the packed instructions
+        float2 e, sl = splat(0.f), sa = splat(0.f), si = splat(0.f);
+        {
+            const float2 m0 = sm.AE[w][lv], m1 = sm.AE[w][lv + V - 1];
+            e = make_float2(fmaf(m0.x, sm.c.in[lv], m0.y), fmaf(m1.x, sm.c.in[lv + V - 1], m1.y));
+        }
+#pragma unroll
+        for (int k = S - 1; k >= 0; --k) {
+            hold_loads();
+            float uv[V], gv[V];
+            load_shared<V>(u + k * 32 * V, uv);
+            load_shared<V>(go + k * 32 * V, gv);
+            const float2 pa = make_float2(a[k][0], a[k][V - 1]), pr = make_float2(r[k][0], r[k][V - 1]),
+                         pi = make_float2(i[k][0], i[k][V - 1]), ph = make_float2(x[k][0], x[k][V - 1]),
+                         pu = make_float2(uv[0], uv[V - 1]), pg = make_float2(gv[0], gv[V - 1]);
+            const float2 s = mul2(c, pr);
+            float2 am, om;
+            if (any) decay2<true>(s, am, om);
+            else decay2<false>(s, am, om);
+            const float2 mi = rsqrt2(om);
+            const float2 gt = add2(pg, e), iu = mul2(pi, pu), gm = mul2(gt, mul2(om, mi)), du = mul2(gm, pi);
+            e = mul2(pa, gt);
+            const float2 di = mul2(mul2(gm, iu), fma2(pi, splat(-1.f), splat(1.f)));
+            // ds = e ((a / m) i u - h)
+            const float2 ds = mul2(e, fma2(mul2(pa, mi), iu, mul2(ph, splat(-1.f))));
+            const float2 da = mul2(mul2(ds, s), fma2(pr, splat(-1.f), splat(1.f)));
+            sl = fma2(ds, pr, sl);
+            sa = add2(sa, da);
+            si = add2(si, di);
+            const float ov[3][2] = {{da.x, da.y}, {di.x, di.y}, {du.x, du.y}};
+            T* const to[3] = {ar, ir, u};
+            T* const global[3] = {static_cast<T*>(g.da_raw), static_cast<T*>(g.di_raw), static_cast<T*>(g.du)};
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                float o[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = ov[n][v];
+                if (kTma) store_vec<V>(to[n] + k * 32 * V, o);
+                else if (live && t0 + k < g.L) store_vec<V>(global[n] + (b * g.L + t0 + k) * g.D + d, o);
+            }
+        }
+        if (kTma) fence_proxy_async();
+        const float slv[2] = {sl.x, sl.y}, sav[2] = {sa.x, sa.y}, siv[2] = {si.x, si.y};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float hn = fmaf(a[k][v], h[v], x[k][v]);
-            x[k][v] = h[v];
-            h[v] = hn;
-        }
-    __syncthreads();
-    float e[V], sl[V], sa[V], si[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        e[v] = sIn[lane * V + v];
-        for (int q = kWarps - 1; q > w; --q) e[v] = fmaf(sA[q][lane * V + v], e[v], sE[q][lane * V + v]);
-        sl[v] = sa[v] = si[v] = 0.f;
-    }
-#pragma unroll
-    for (int k = kSteps - 1; k >= 0; --k) {
-        if (!live || t0 + k >= g.L) continue;
-        float uv[V], gv[V], du[V], da[V], di[V];
-        u[k].get(uv);
-        go[k].get(gv);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float s = sRate[lane * V + v] * r[k][v];
-            float am, om;
-            decay(s, am, om);
-            const float mi = om > 0.f ? rsqrt_fast(om) : 0.f;  // 1 / m
-            const float gt = gv[v] + e[v];
-            e[v] = a[k][v] * gt;
-            du[v] = gt * (om * mi) * i[k][v];
-            di[v] = du[v] * uv[v] * (1.f - i[k][v]);
-            const float ds = -e[v] * (x[k][v] - am * mi * i[k][v] * uv[v]);
-            da[v] = ds * s * (1.f - r[k][v]);
-            sl[v] = fmaf(ds, r[k][v], sl[v]);
-            sa[v] += da[v];
-            si[v] += di[v];
-        }
-        store_vec<V>(static_cast<T*>(g.du) + base + k * g.D, du);
-        store_vec<V>(static_cast<T*>(g.da_raw) + base + k * g.D, da);
-        store_vec<V>(static_cast<T*>(g.di_raw) + base + k * g.D, di);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        red[0][w][lane * V + v] = sl[v];
-        red[1][w][lane * V + v] = sa[v];
-        red[2][w][lane * V + v] = si[v];
-    }
-    __syncthreads();
-    if (w < 3 && live) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float s = 0.f;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) s += red[w][q][lane * V + v];
-            g.part[((b * g.chain.tiles + j) * 3 + w) * g.D + d + v] = s;
+            sm.red[0][w][lv + v] = slv[v];
+            sm.red[1][w][lv + v] = sav[v];
+            sm.red[2][w][lv + v] = siv[v];
         }
     }
+    if (kTma && w == kWarps + 1 && lane == 0) tma_store_wait_all();
 }
 
 template <typename T, int V>
@@ -465,11 +792,19 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
     load_vec<V>(static_cast<const T*>(g.i_raw) + at, ir);
     hs.get(h);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float a, om;
-        const float ab = g.a_bias ? __ldg(g.a_bias + d + v) : 0.f, ib = g.i_bias ? __ldg(g.i_bias + d + v) : 0.f;
-        decay(decay_rate(__ldg(g.Lam + d + v), g.rate) * sigmoid(ar[v] + ab), a, om);
-        h[v] = fmaf(a, h[v], sqrt_fast(om) * sigmoid(ir[v] + ib) * u[v]);
+    for (int v = 0; v < V; v += 2) {
+        // V = 1 computes its one element twice
+        const int v1 = V == 1 ? 0 : v + 1;
+        float2 r, i, a, om, nab = splat(0.f), nib = splat(0.f);
+        if (g.a_bias) nab = make_float2(-kLog2e * __ldg(g.a_bias + d + v), -kLog2e * __ldg(g.a_bias + d + v1));
+        if (g.i_bias) nib = make_float2(-kLog2e * __ldg(g.i_bias + d + v), -kLog2e * __ldg(g.i_bias + d + v1));
+        const float2 c = make_float2(decay_rate(__ldg(g.Lam + d + v), g.rate), decay_rate(__ldg(g.Lam + d + v1), g.rate));
+        gates2(make_float2(ar[v], ar[v1]), make_float2(ir[v], ir[v1]), nab, nib, r, i);
+        decay2<true>(mul2(c, r), a, om);
+        const float2 m = mul2(om, rsqrt2(om));
+        const float2 hn = fma2(a, make_float2(h[v], h[v1]), mul2(mul2(m, i), make_float2(u[v], u[v1])));
+        h[v] = hn.x;
+        if (V > 1) h[v1] = hn.y;
     }
     hs.set(h);
     hs.store(g.state + at);
@@ -503,86 +838,137 @@ sscan_status check_gated(const sscan_gated_problem* p) {
         return api_fail(SSCAN_ERR_INVALID_ARG, "rate must be in (0, 1e6]");
     if (sscan_status s = api_elements(p->batch, p->seqlen, p->dim)) return s;
     // tickets are 32-bit counts of tiles (of 32 channels at least)
-    const int64_t tiles = (p->seqlen + kTile - 1) / kTile, blocks = p->batch * ((p->dim + 31) / 32);
-    if (tiles > 0 && blocks > ((int64_t(1) << 31) - 1) / tiles)
-        return api_fail(SSCAN_ERR_UNSUPPORTED, "more than 2^31 tiles of %d steps by 32 channels", kTile);
+    // (and the steps of a sequence, which TMA coordinates count)
+    const int64_t tiles = (p->seqlen + kCkpt - 1) / kCkpt, blocks = p->batch * ((p->dim + 31) / 32);
+    if (tiles > 0 && blocks > ((int64_t(1) << 31) - 4096) / tiles)
+        return api_fail(SSCAN_ERR_UNSUPPORTED, "more than 2^31 tiles of %d steps by 32 channels", kCkpt);
+    if (p->seqlen > (int64_t(1) << 31) - 4096 || p->dim > (int64_t(1) << 31) - 4096 || p->batch > (int64_t(1) << 31) - 1)
+        return api_fail(SSCAN_ERR_UNSUPPORTED, "a size of 2^31 or more");
     return SSCAN_OK;
 }
 
-int64_t gated_tiles(const sscan_gated_problem* p) { return (p->seqlen + kTile - 1) / kTile; }
+int64_t gated_tiles(const sscan_gated_problem* p, int steps) {
+    return (p->seqlen + kWarps * steps - 1) / (kWarps * steps);
+}
+int64_t gated_ckpts(const sscan_gated_problem* p) { return gated_tiles(p, kStepsBwd); }
 
-// The chain's arrays for column blocks of 32 channels (the most there can be): counters first,
-// since they are cleared together before each launch.  Channel blocks of 64 use the same
-// space, half as many columns of twice the width.
+// The chain's arrays, for column blocks of 32 channels or of 64, half as many of twice the width.
 struct ChainLayout {
-    size_t counters, maps, states, bytes;  // byte offsets and total
+    size_t maps, groups, states, bytes;  // byte offsets, and the whole
 };
 
-ChainLayout chain_layout(const sscan_gated_problem* p) {
+ChainLayout chain_layout(const sscan_gated_problem* p, int steps) {
     ChainLayout l{};
-    const size_t tiles = (size_t)gated_tiles(p), cols = (size_t)(p->batch * ((p->dim + 63) / 64 * 2));
+    const size_t tiles = (size_t)gated_tiles(p, steps), words = (size_t)(p->batch * ((p->dim + 63) / 64 * 64)) * 8;
     if (tiles <= 1) return l;
-    const size_t groups = (tiles + kGroup - 1) / kGroup;
-    l.counters = round256((1 + cols * (tiles + groups)) * sizeof(unsigned int));
-    l.maps = l.counters;
-    l.states = l.maps + round256(cols * tiles * 32 * sizeof(float2));
-    l.bytes = l.states + round256(cols * groups * 32 * sizeof(float));
+    const size_t groups = (tiles + kFan - 1) / kFan, supers = (groups + kFan - 1) / kFan;
+    l.maps = 256;  // the ticket before it
+    l.groups = l.maps + words * tiles;
+    l.states = l.groups + words * groups;
+    l.bytes = round256(l.states + words * supers);
     return l;
 }
 
 size_t gated_ckpt_bytes(const sscan_gated_problem* p) {
-    return round256((size_t)(p->batch * gated_tiles(p) * p->dim) * sizeof(float));
+    return round256((size_t)(p->batch * gated_ckpts(p) * p->dim) * sizeof(float));
 }
 
 bool empty(const sscan_gated_problem* p) { return p->batch == 0 || p->seqlen == 0 || p->dim == 0; }
 
-// Two channels per lane where every pointer and the width allow it.
-int gated_width(const GatedArgs& g, size_t es) {
-    if (g.D % 2) return 1;
-    for (const void* p : {g.u, g.a_raw, g.i_raw, (const void*)g.out, g.dout, (const void*)g.du,
-                          (const void*)g.da_raw, (const void*)g.di_raw})
-        if (!aligned_to(p, 2 * es)) return 1;
-    return 2;
-}
-
-cudaError_t set_chain(GatedArgs& g, const sscan_gated_problem* p, void* ws, int V, cudaStream_t st) {
+cudaError_t set_chain(GatedArgs& g, const sscan_gated_problem* p, void* ws, int V, int steps, cudaStream_t st) {
     Chain& c = g.chain;
-    c.tiles = gated_tiles(p);
+    c.tiles = gated_tiles(p, steps);
     g.nblk = (p->dim + 32 * V - 1) / (32 * V);
     c.cols = p->batch * g.nblk;
-    c.groups = (c.tiles + kGroup - 1) / kGroup;
+    c.ngroups = (c.tiles + kFan - 1) / kFan;
+    c.nsupers = (c.ngroups + kFan - 1) / kFan;
     if (c.tiles <= 1) return cudaSuccess;
-    const ChainLayout l = chain_layout(p);
+    const ChainLayout l = chain_layout(p, steps);
     char* base = static_cast<char*>(ws);
     c.ticket = reinterpret_cast<unsigned int*>(base);
-    c.mapped = c.ticket + 1;
-    c.entered = c.mapped + c.cols * c.tiles;
-    c.maps = reinterpret_cast<float2*>(base + l.maps);
-    c.states = reinterpret_cast<float*>(base + l.states);
-    return cudaMemsetAsync(base, 0, l.counters, st);
+    c.maps = reinterpret_cast<unsigned long long*>(base + l.maps);
+    c.groups = reinterpret_cast<unsigned long long*>(base + l.groups);
+    c.states = reinterpret_cast<unsigned long long*>(base + l.states);
+    return cudaMemsetAsync(base, 0xff, l.bytes, st);
 }
 
-template <typename T>
-void launch_gated(const GatedArgs& g, bool bwd, int V, cudaStream_t st) {
-    const unsigned blocks = (unsigned)(g.chain.cols * g.chain.tiles);
+// A map over a (batch, L, D) tensor with boxes of `rows` steps by 32 V channels.
+template <typename T, int V>
+bool gated_map(CUtensorMap* m, const void* base, const GatedArgs& g, int rows) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.D, (cuuint64_t)g.L, (cuuint64_t)g.batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)(g.D * sizeof(T)), (cuuint64_t)(g.L * g.D * sizeof(T))};
+    const cuuint32_t box[3] = {32 * V, (cuuint32_t)rows, 1}, each[3] = {1, 1, 1};
+    return fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+              const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks that the GPU holds at once; fewer tiles take fewer.
+constexpr int64_t kSms = 148;
+
+template <typename T, int V, bool kTma>
+cudaError_t launch_gated(const GatedArgs& g, bool bwd, cudaStream_t st) {
+    const int64_t all = g.chain.cols * g.chain.tiles, hold = (sizeof(T) == 2 ? 2 : 1) * kSms;
+    const unsigned blocks = (unsigned)(all < hold ? all : hold);
+    CUtensorMap m[7] = {};
+    cudaError_t e;
     if (bwd) {
-        if (V == 2) gated_bwd_kernel<T, 2><<<blocks, 32 * kWarps, 0, st>>>(g);
-        else gated_bwd_kernel<T, 1><<<blocks, 32 * kWarps, 0, st>>>(g);
+        const void* t[7] = {g.a_raw, g.i_raw, g.u, g.dout, g.da_raw, g.di_raw, g.du};
+        if (kTma)
+            for (int i = 0; i < 7; ++i)
+                if (!gated_map<T, V>(&m[i], t[i], g, kWarps * kStepsBwd)) return cudaErrorInvalidValue;
+        constexpr size_t smem = sizeof(GatedBwdSmem<T, V>);
+        e = cudaFuncSetAttribute(gated_bwd_kernel<T, V, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        gated_bwd_kernel<T, V, kTma><<<blocks, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], g);
     } else {
-        if (V == 2) gated_fwd_kernel<T, 2><<<blocks, 32 * kWarps, 0, st>>>(g);
-        else gated_fwd_kernel<T, 1><<<blocks, 32 * kWarps, 0, st>>>(g);
+        const void* t[4] = {g.a_raw, g.i_raw, g.u, g.out ? g.out : g.u};
+        if (kTma)
+            for (int i = 0; i < 4; ++i)
+                if (!gated_map<T, V>(&m[i], t[i], g, kWarps * kStepsFwd)) return cudaErrorInvalidValue;
+        constexpr size_t smem = sizeof(GatedSmem<T, V, 3, kStepsFwd>);
+        e = cudaFuncSetAttribute(gated_fwd_kernel<T, V, kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        gated_fwd_kernel<T, V, kTma><<<blocks, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], g);
     }
     api_count_launch();
+    return cudaGetLastError();
+}
+
+// Two channels per lane where every pointer and the width allow it, by TMA where they are on
+// 16-byte boundaries.
+template <typename T>
+cudaError_t launch_width(const GatedArgs& g, int V, bool tma, bool bwd, cudaStream_t st) {
+    if (V == 1) return launch_gated<T, 1, false>(g, bwd, st);
+    return tma ? launch_gated<T, 2, true>(g, bwd, st) : launch_gated<T, 2, false>(g, bwd, st);
 }
 
 sscan_status run_gated(GatedArgs& g, const sscan_gated_problem* p, void* ws, bool bwd, cudaStream_t st) {
-    const bool bf16 = p->io_dtype == SSCAN_BF16;
-    const int V = gated_width(g, bf16 ? 2 : 4);
-    const cudaError_t e = set_chain(g, p, ws, V, st);
-    if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "clearing the carry's counters: %s", cudaGetErrorString(e));
-    if (bf16) launch_gated<__nv_bfloat16>(g, bwd, V, st);
-    else launch_gated<float>(g, bwd, V, st);
-    return api_launched(bwd ? "gated backward kernel" : "gated forward kernel");
+    const size_t es = p->io_dtype == SSCAN_BF16 ? 2 : 4;
+    auto all_aligned = [&](size_t n) {
+        for (const void* q : {g.u, g.a_raw, g.i_raw, (const void*)g.out, g.dout, (const void*)g.du,
+                              (const void*)g.da_raw, (const void*)g.di_raw})
+            if (!aligned_to(q, n)) return false;
+        return g.D * es % n == 0;
+    };
+    const int V = all_aligned(2 * es) ? 2 : 1;
+    cudaError_t e = set_chain(g, p, ws, V, bwd ? kStepsBwd : kStepsFwd, st);
+    if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "clearing the carry's words: %s", cudaGetErrorString(e));
+    const bool tma = all_aligned(16);
+    e = es == 2 ? launch_width<__nv_bfloat16>(g, V, tma, bwd, st) : launch_width<float>(g, V, tma, bwd, st);
+    if (e != cudaSuccess)
+        return api_fail(SSCAN_ERR_CUDA, "gated %s kernel: %s", bwd ? "backward" : "forward", cudaGetErrorString(e));
+    return SSCAN_OK;
 }
 
 GatedArgs gated_args(const sscan_gated_problem* p, const void* u, const void* a_raw, const void* i_raw,
@@ -618,16 +1004,17 @@ using namespace sscan;
 extern "C" {
 
 int64_t sscan_gated_checkpoints(const sscan_gated_problem* p) {
-    return check_gated(p) == SSCAN_OK ? gated_tiles(p) : 0;
+    return check_gated(p) == SSCAN_OK ? gated_ckpts(p) : 0;
 }
 
 size_t sscan_gated_workspace_size(const sscan_gated_problem* p, int op) {
     if (check_gated(p) != SSCAN_OK || empty(p)) return 0;
-    const size_t chain = chain_layout(p).bytes;
-    if (op == SSCAN_OP_FWD) return chain;
+    const size_t fwd = chain_layout(p, kStepsFwd).bytes, bwd = chain_layout(p, kStepsBwd).bytes;
+    if (op == SSCAN_OP_FWD) return fwd;
     if (op != SSCAN_OP_BWD) return 0;
     // the carry, one row of partial sums per tile, and the checkpoints when the caller has none
-    return chain + round256((size_t)(p->batch * gated_tiles(p) * 3 * p->dim) * sizeof(float)) + gated_ckpt_bytes(p);
+    return (fwd > bwd ? fwd : bwd) + round256((size_t)(p->batch * gated_ckpts(p) * 3 * p->dim) * sizeof(float)) +
+           gated_ckpt_bytes(p);
 }
 
 sscan_status sscan_gated_fwd(const sscan_gated_problem* p, const void* u, const void* a_raw, const void* i_raw,
@@ -676,7 +1063,8 @@ sscan_status sscan_gated_bwd(const sscan_gated_problem* p, const void* u, const 
     if (!u || !a_raw || !i_raw || !Lam || !dout || !du || !da_raw || !di_raw)
         return api_fail(SSCAN_ERR_INVALID_ARG, "u, a_raw, i_raw, Lam, dout, du, da_raw and di_raw are required");
     if (sscan_status s = api_workspace(sscan_gated_workspace_size(p, SSCAN_OP_BWD), workspace, workspace_bytes)) return s;
-    const size_t chain = chain_layout(p).bytes;
+    const size_t fwd = chain_layout(p, kStepsFwd).bytes, bwd = chain_layout(p, kStepsBwd).bytes;
+    const size_t chain = fwd > bwd ? fwd : bwd;
     float* ckpt = reinterpret_cast<float*>(static_cast<char*>(workspace) + chain);
     GatedArgs g = gated_args(p, u, a_raw, i_raw, Lam, a_bias, i_bias, h0);
     if (!checkpoints) {
@@ -688,7 +1076,7 @@ sscan_status sscan_gated_bwd(const sscan_gated_problem* p, const void* u, const 
     g.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ckpt) + gated_ckpt_bytes(p));
     g.dout = dout, g.du = du, g.da_raw = da_raw, g.di_raw = di_raw, g.dh0 = dh0;
     if (sscan_status s = run_gated(g, p, workspace, true, st)) return s;
-    launch_rowsum(g.part, p->batch * gated_tiles(p), 3 * p->dim,
+    launch_rowsum(g.part, p->batch * gated_ckpts(p), 3 * p->dim,
                   GatedGradPut{dLam, da_bias, di_bias, Lam, p->rate, p->dim}, st);
     api_count_launch();
     return api_launched("gated gradient sum");

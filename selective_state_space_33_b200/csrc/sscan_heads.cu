@@ -280,11 +280,11 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                 for (int k = 0; k < 2; ++k) {
                     const int at = (k ? tb : ta) * PP + c_p + 8 * j + 2 * q;
                     float xv[2], v[2] = {y[j][2 * k], y[j][2 * k + 1]};
-                    load_shared2(t.x + at, xv);
+                    load_shared<2>(t.x + at, xv);
                     if (a.D) v[0] = fmaf(D, xv[0], v[0]), v[1] = fmaf(D, xv[1], v[1]);
                     if (z) {
                         float zv[2];
-                        load_shared2(sm.z + at, zv);
+                        load_shared<2>(sm.z + at, zv);
                         v[0] *= silu(zv[0]), v[1] *= silu(zv[1]);
                     }
                     store_vec<2>(sm.z + at, v);

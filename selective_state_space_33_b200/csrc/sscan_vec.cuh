@@ -66,10 +66,10 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[V]) {
     t.get(x);
 }
 
-// Two neighbouring elements of a shared-memory tile.
-template <typename T>
-__device__ __forceinline__ void load_shared2(const T* p, float (&x)[2]) {
-    Vec<T, 2> t;
+// V neighbouring elements of a shared-memory tile.
+template <int V, typename T>
+__device__ __forceinline__ void load_shared(const T* p, float (&x)[V]) {
+    Vec<T, V> t;
     t.load_rw(p);
     t.get(x);
 }

@@ -227,22 +227,22 @@ def test_binding_refuses_on_device(cuda_device):
         with pytest.raises(sb.SscanError, match="rate"):
             sb.sscan_gated_fwd(u, a, i, lam, rate=rate)
     with pytest.raises(sb.SscanError, match="workspace"):
-        sb.sscan_gated_fwd(u, a, i, lam, workspace=torch.empty(256, dtype=torch.uint8, device=cuda_device)[:16])
+        sb.sscan_gated_bwd(u, a, i, lam, u, workspace=torch.empty(256, dtype=torch.uint8, device=cuda_device)[:16])
 
 
 def test_c_entry_refuses():
     lib = sb.load_library()
     fake = ctypes.c_void_p(0x10000)
-    ok = sb.GatedProblem(2, 100, 6, 0, 8.0)
+    ok = sb.GatedProblem(2, 200, 6, 0, 8.0)
     assert lib.sscan_gated_fwd(None, *([fake] * 10), fake, 1 << 20, None) == 1
     assert lib.sscan_gated_fwd(sb.GatedProblem(2, -1, 6, 0, 8.0), *([fake] * 10), fake, 1 << 20, None) == 1
     assert lib.sscan_gated_fwd(sb.GatedProblem(2, 100, 6, 3, 8.0), *([fake] * 10), fake, 1 << 20, None) == 1
     assert lib.sscan_gated_fwd(sb.GatedProblem(1 << 20, 1 << 17, 64, 0, 8.0), *([fake] * 10), fake, 1 << 20, None) == 2
     need = lib.sscan_gated_workspace_size(ok, sb.SSCAN_OP_FWD)
     assert need > 0 and need % 256 == 0
-    # one tile of 64 steps needs no carry
+    # one tile needs no carry
     assert lib.sscan_gated_workspace_size(sb.GatedProblem(2, 64, 6, 0, 8.0), sb.SSCAN_OP_FWD) == 0
-    assert lib.sscan_gated_checkpoints(ok) == 2
+    assert lib.sscan_gated_checkpoints(ok) == 4
     assert lib.sscan_gated_fwd(ok, *([fake] * 10), None, 0, None) == 3
     assert lib.sscan_gated_fwd(ok, *([fake] * 10), fake, need - 1, None) == 3
     assert lib.sscan_gated_fwd(ok, fake, None, *([fake] * 8), fake, need, None) == 1
