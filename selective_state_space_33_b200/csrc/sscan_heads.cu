@@ -49,7 +49,7 @@ struct Walk {
         alignas(16) T z[out ? kQ * PITCH_P : 8];             // the gate, then the outputs
         alignas(16) T sh[out ? kHeadDim * PITCH_N : 8];      // the state, [p][n]
         alignas(16) T sl[out && bf16 ? kHeadDim * PITCH_N : 8];
-        alignas(16) T fb[scale_b ? 3 : 1][scale_b ? kQ * PITCH_N : 8];  // f B in three parts
+        alignas(16) T fb[scale_b ? 3 : 1][scale_b ? kQ * NT : 8];  // f B in three parts
         ChunkScalars s[2];
     };
 };
@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
         __syncthreads();      // this chunk's tiles and scalars are here; with two buffers, the other one is free
         const ChunkScalars& sc = sm.s[i & 1];
         if constexpr (W::out) {
+            // the gate: a warp's own 16 steps (and, with two warps on them, both halves)
             if (z)
-                load_tile_async<T, kHeadDim>(sm.z, PP, z + row * a.P, (int64_t)a.H * a.P, rows, a.P, a.vec, tid, kWork);
+                load_rows_async<T>(sm.z + p0 * PP, PP, z + (row + (int64_t)p0 * a.H) * a.P, (int64_t)a.H * a.P, rows - p0,
+                                   a.P, a.vec);
             cp_async_commit();
         }
         if (W::stages == 2) {
@@ -221,20 +223,13 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                 for (int k = 0; k < 2; ++k) {
                     const int at = (p0 + g + 8 * k) * PN + n0 + 8 * j + 2 * q;
                     const float x = S[j][2 * k], y = S[j][2 * k + 1];
-                    if constexpr (W::bf16) {
-                        const uint32_t hi = M::pack(x, y);
-                        *reinterpret_cast<uint32_t*>(sm.sh + at) = hi;
-                        *reinterpret_cast<uint32_t*>(sm.sl + at) =
-                            M::pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-                    } else {
-                        *reinterpret_cast<float2*>(sm.sh + at) = make_float2(x, y);
-                    }
+                    split_store2<T>(sm.sh, sm.sl, at, x, y);
                 }
             if constexpr (W::scale_b) {
 #pragma unroll
                 for (int k = tid; k < kQ * NT / 2; k += kWork) {
-                    const int s = k / (NT / 2), at = s * PN + (k - s * (NT / 2)) * 2;
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(t.B + at);
+                    const int s = k / (NT / 2), n = (k - s * (NT / 2)) * 2, at = s * NT + n;
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(t.B + s * PN + n);
                     float x = __uint_as_float(v << 16) * sc.f[s], y = __uint_as_float(v & 0xffff0000u) * sc.f[s];
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
@@ -272,7 +267,8 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             // skip term and gate, through the gate's own rows of shared memory to 16-byte stores
             if (W::stages == 2) cp_async_wait<1>();
             else cp_async_wait<0>();
-            product_sync<kWork>();
+            if (WC > 1) product_sync<kWork>();
+            else __syncwarp();
             const float D = a.D ? __ldg(a.D + h) : 0.f;
 #pragma unroll
             for (int j = 0; j < PTL; ++j)
@@ -323,7 +319,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
 #pragma unroll
                     for (int j = 0; j < NTL; j += 2) {
                         typename M::B b0, b1;
-                        M::load_bt2(b0, b1, sm.fb[part], PN, n0 + 8 * j, k);
+                        M::load_bt2(b0, b1, sm.fb[part], NT, n0 + 8 * j, k);
                         M::mma(part ? lo[j] : hi[j], fa, b0);
                         M::mma(part ? lo[j + 1] : hi[j + 1], fa, b1);
                     }
@@ -639,6 +635,7 @@ sscan_status sscan_heads_fwd(const sscan_heads_problem* p, const void* u, const 
     if (sscan_status s = api_workspace(sscan_heads_workspace_size(p, SSCAN_OP_FWD), workspace, workspace_bytes)) return s;
     HeadsArgs a = heads_args(p, u, delta_raw, delta_bias, A, B, C, D_skip, z, h0);
     a.out = out, a.h_last = h_last;
+    a.vec = a.vec && aligned_to(z, 16) && aligned_to(out, 16);
     plan_heads(a);
     const bool bf16 = p->io_dtype == SSCAN_BF16;
     cudaError_t e = cudaSuccess;

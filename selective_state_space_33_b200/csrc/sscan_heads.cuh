@@ -45,13 +45,18 @@ struct alignas(16) ChunkScalars {
     float e[kQ];              // exp(c_t)
     float d[kQ];              // exp(c_end - c_t)
     float f[kQ];              // d_t w_t
-    float dl[kQ], raw[kQ];    // step sizes, and what softplus was taken of
     float total;              // c_end
 };
 
-// One warp fills s for steps t0 .. t0 + kQ - 1 of (b, h); past L: q = w = 0.
+// What the gradients of the scalars need besides.
+struct ChunkSteps {
+    float dl[kQ], raw[kQ];    // step sizes, and what softplus was taken of
+};
+
+// One warp fills s (and steps) for steps t0 .. t0 + kQ - 1 of (b, h); past L: q = w = 0.
 template <typename T>
-__device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& a, int64_t b, int h, int64_t t0) {
+__device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& a, int64_t b, int h, int64_t t0,
+                                              ChunkSteps* steps = nullptr) {
     const int lane = threadIdx.x & 31;
     const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
     const T* dr = static_cast<const T*>(a.delta_raw);
@@ -62,15 +67,14 @@ __device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& 
         const int64_t t = t0 + 2 * lane + i;
         c[i] = 0.0;
         w[i] = 0.f;
-        s.dl[2 * lane + i] = s.raw[2 * lane + i] = 0.f;
+        if (steps) steps->dl[2 * lane + i] = steps->raw[2 * lane + i] = 0.f;
         if (t < a.L) {
             const float r = IO<T>::load(dr, (b * a.L + t) * a.H + h) + bias;
             const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
             const float q = dl * A;
             w[i] = A != 0.f ? expm1f(q) / A : dl;
             c[i] = q < -1e4f ? -1e4 : (double)q;  // exp(-1e4) is 0 in fp32; keeps sums finite
-            s.dl[2 * lane + i] = dl;
-            s.raw[2 * lane + i] = r;
+            if (steps) steps->dl[2 * lane + i] = dl, steps->raw[2 * lane + i] = r;
         }
     }
     c[1] += c[0];
@@ -142,14 +146,38 @@ __device__ __forceinline__ void load_tile_async(T* dst, int pitch, const T* src,
     }
 }
 
-// x as hi + lo in the tile type: bf16 keeps 16 bits in the two (a relative 2^-17), which is
-// what an fp32 state or gradient needs from a factor that is not itself a bf16 input; an
-// fp32 tile needs no second part.
+// 16 rows of kHeadDim elements by one warp, likewise.
 template <typename T>
-__device__ __forceinline__ void split_store(T* hi, T* lo, int at, float x) {
-    const T h = from_f32<T>(x);
-    hi[at] = h;
-    if constexpr (!Mma<T>::kExact32) lo[at] = from_f32<T>(x - to_f32<T>(h));
+__device__ __forceinline__ void load_rows_async(T* dst, int pitch, const T* src, int64_t stride, int64_t rows, int cols,
+                                                bool vec) {
+    constexpr int VE = 16 / sizeof(T), PER = kHeadDim / VE;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = lane; i < 16 * PER; i += 32) {
+        const int r = i / PER, c = (i - r * PER) * VE;
+        if (vec) {
+            const bool in = r < rows && c < cols;
+            cp_async16(dst + r * pitch + c, in ? src + r * stride + c : src, in);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VE; ++j) dst[r * pitch + c + j] = r < rows && c + j < cols ? src[r * stride + c + j] : from_f32<T>(0.f);
+        }
+    }
+}
+
+// Neighbouring values x, y as hi + lo in the tile type: bf16 keeps 16 bits in the two (a relative
+// 2^-17), which is what an fp32 sum needs from a factor that is not itself a bf16 input; an fp32
+// tile needs no second part.
+template <typename T>
+__device__ __forceinline__ void split_store2(T* hi, T* lo, int at, float x, float y) {
+    if constexpr (Mma<T>::kExact32) {
+        *reinterpret_cast<float2*>(hi + at) = make_float2(x, y);
+    } else {
+        const uint32_t h = Mma<T>::pack(x, y);
+        *reinterpret_cast<uint32_t*>(hi + at) = h;
+        *reinterpret_cast<uint32_t*>(lo + at) =
+            Mma<T>::pack(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
+    }
 }
 
 template <typename T, int NT> struct HeadsPitch {

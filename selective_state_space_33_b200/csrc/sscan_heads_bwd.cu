@@ -55,6 +55,7 @@ struct BwdSmem {
     alignas(16) T m1[kQ * Pt::Q];                // [t][s]
     alignas(16) T m2[kQ * Pt::Q];
     ChunkScalars s;
+    ChunkSteps steps;
     float row[2][kQ], col[4][kQ], qs[2][kQ], rs[2][kQ];
     float sum[2][kThreads / 32];
 };
@@ -104,13 +105,13 @@ __device__ __forceinline__ void load_state(T* hi, T* lo, const float* src, int P
             }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) split_store<T>(hi, lo, p * pitch + n + k, v[k]);
+        for (int k = 0; k < 4; k += 2) split_store2<T>(hi, lo, p * pitch + n + k, v[k], v[k + 1]);
         each(i, v);
     }
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
+__global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 1) heads_bwd_kernel(HeadsBwdArgs k) {
     using Pt = HeadsPitch<T, NT>;
     using M = Mma<T>;
     constexpr int NTL = NT / 8, HTL = NTL > 8 ? 8 : NTL;  // dB / dC columns in passes of at most 64
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
     for (int h = h_begin; h < h_end; ++h) {
         const int64_t bh = b * a.H + h;
         const float D = a.D ? __ldg(a.D + h) : 0.f;
-        if (w == 0) chunk_scalars<T>(sm.s, a, b, h, t0);
+        if (w == 0) chunk_scalars<T>(sm.s, a, b, h, t0, &sm.steps);
         // u, dy and their product's sum
         float dsum = 0.f, ssum = 0.f;
         {
@@ -166,10 +167,10 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < VE; ++j) {
-                    if (z) dv[j] *= silu(zv[j]);
-                    dsum = fmaf(dv[j], xv[j], dsum);
-                    split_store<T>(sm.dyh, sm.dyl, t * Pt::P + p + j, dv[j]);
+                for (int j = 0; j < VE; j += 2) {
+                    if (z) dv[j] *= silu(zv[j]), dv[j + 1] *= silu(zv[j + 1]);
+                    dsum = fmaf(dv[j], xv[j], fmaf(dv[j + 1], xv[j + 1], dsum));
+                    split_store2<T>(sm.dyh, sm.dyl, t * Pt::P + p + j, dv[j], dv[j + 1]);
                 }
                 store_vec<VE>(sm.x + t * Pt::P + p, xv);
             }
@@ -197,6 +198,37 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
         if (lane == 0) sm.sum[0][w] = dsum, sm.sum[1][w] = ssum;
         __syncthreads();
 
+        // A warp's 16 rows by 32 columns of du or dz, by way of its own part of dyl (read before) to
+        // 16-byte stores; fp32 has no dyl and stores its pairs.
+        auto store_part = [&](T* out, const float (&v)[4][4]) {
+            if (!M::kExact32 && a.vec) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo[2] = {v[j][0], v[j][1]}, hi[2] = {v[j][2], v[j][3]};
+                    store_vec<2>(sm.dyl + ra * Pt::P + cb + 8 * j, lo);
+                    store_vec<2>(sm.dyl + rb * Pt::P + cb + 8 * j, hi);
+                }
+                __syncwarp();
+                constexpr int VE = 16 / sizeof(T), PER = 32 / VE;
+#pragma unroll
+                for (int i = lane; i < 16 * PER; i += 32) {
+                    const int t = 16 * wr + i / PER, p = 32 * wc + (i % PER) * VE;
+                    if (t < rows && p < a.P)
+                        *reinterpret_cast<uint4*>(out + ((tok + t) * a.H + h) * a.P + p) =
+                            *reinterpret_cast<const uint4*>(sm.dyl + t * Pt::P + p);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = i < 2 ? ra : rb, p = cb + 8 * j + (i & 1);
+                        if (t < rows && p < a.P) out[((tok + t) * a.H + h) * a.P + p] = from_f32<T>(v[j][i]);
+                    }
+            }
+        };
+
         // H, then M1, M2 and the sums of G H E over rows and columns
         float Hm[4][4];
         zero_acc(Hm);
@@ -208,24 +240,33 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
         float rowa = 0.f, rowb = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const int s0 = cb + 8 * j;
+            const float2 ws = *reinterpret_cast<const float2*>(sm.s.w + s0);
             float cols[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = i < 2 ? ra : rb, s = cb + 8 * j + (i & 1);
-                const float E = s <= t ? chunk_decay(sm.s, t, s) : 0.f;
-                const float ge = s <= t ? G[j][i] * E : 0.f, he = s <= t ? Hm[j][i] * E : 0.f, ws = sm.s.w[s];
-                const float pair = s <= t ? ge * Hm[j][i] : 0.f;
-                cols[i & 1] += pair;
-                (i < 2 ? rowa : rowb) += pair * ws;
-                sm.m1[t * Pt::Q + s] = from_f32<T>(ge * ws);
-                sm.m2[t * Pt::Q + s] = from_f32<T>(he * ws);
+            for (int i = 0; i < 4; i += 2) {
+                const int t = i ? rb : ra;
+                float m1[2], m2[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float E = chunk_decay(sm.s, t, s0 + n), w_ = n ? ws.y : ws.x;
+                    const bool in = s0 + n <= t;
+                    const float ge = in ? G[j][i + n] * E : 0.f, he = in ? Hm[j][i + n] * E : 0.f;
+                    const float pair = in ? ge * Hm[j][i + n] : 0.f;
+                    cols[n] += pair;
+                    (i ? rowb : rowa) += pair * w_;
+                    m1[n] = ge * w_;
+                    m2[n] = he * w_;
+                }
+                store_vec<2>(sm.m1 + t * Pt::Q + s0, m1);
+                store_vec<2>(sm.m2 + t * Pt::Q + s0, m2);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float v = cols[i];
 #pragma unroll
                 for (int o = 4; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (g == 0) sm.col[wr][cb + 8 * j + i] = v;
+                if (g == 0) sm.col[wr][s0 + i] = v;
             }
         }
         rowa = quad_sum(rowa);
@@ -233,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
         if (q == 0) sm.row[wc][ra] = rowa, sm.row[wc][rb] = rowb;
         __syncthreads();
 
-        // du: rows s, columns p
+        // du: rows s, columns p; then S C and, with a gate, dz
         {
             float x[4][4];
             zero_acc(x);
@@ -241,62 +282,76 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
             if constexpr (!M::kExact32)
                 warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.rl, Pt::N, 32 * wc, 0, NT);
             float va = 0.f, vb = 0.f;
+            const float fa = sm.s.f[ra], fb = sm.s.f[rb];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s = i < 2 ? ra : rb;
-                    (i < 2 ? va : vb) += x[j][i] * to_f32<T>(sm.x[s * Pt::P + cb + 8 * j + (i & 1)]);
-                    x[j][i] *= sm.s.f[s];
-                }
+            for (int j = 0; j < 4; ++j) {
+                float u0[2], u1[2];
+                load_shared<2>(sm.x + ra * Pt::P + cb + 8 * j, u0);
+                load_shared<2>(sm.x + rb * Pt::P + cb + 8 * j, u1);
+                va = fmaf(x[j][0], u0[0], fmaf(x[j][1], u0[1], va));
+                vb = fmaf(x[j][2], u1[0], fmaf(x[j][3], u1[1], vb));
+                x[j][0] *= fa, x[j][1] *= fa;
+                x[j][2] *= fb, x[j][3] *= fb;
+            }
             va = quad_sum(va);
             vb = quad_sum(vb);
             if (q == 0) sm.rs[wc][ra] = va, sm.rs[wc][rb] = vb;
             warp_gemm<T, true, true, 4>(x, sm.m1, Pt::Q, 16 * wr, sm.dyh, Pt::P, 32 * wc, 16 * wr, kQ);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s = i < 2 ? ra : rb, p = cb + 8 * j + (i & 1);
-                    if (s >= rows || p >= a.P) continue;
-                    float dy = to_f32<T>(sm.dyh[s * Pt::P + p]);
-                    if constexpr (!M::kExact32) dy += to_f32<T>(sm.dyl[s * Pt::P + p]);
-                    static_cast<T*>(k.du)[((tok + s) * a.H + h) * a.P + p] = from_f32<T>(fmaf(D, dy, x[j][i]));
-                }
-        }
-        // S C and, with a gate, dz: rows t, columns p
-        {
+            // S C: rows t, columns p
             float y[4][4];
             zero_acc(y);
             warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
             if constexpr (!M::kExact32)
                 warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sl, Pt::N, 32 * wc, 0, NT);
-            float va = 0.f, vb = 0.f;
+            const float ea = sm.s.e[ra], eb = sm.s.e[rb];
+            va = vb = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = i < 2 ? ra : rb, p = cb + 8 * j + (i & 1);
-                    float dy = to_f32<T>(sm.dyh[t * Pt::P + p]);
-                    if constexpr (!M::kExact32) dy += to_f32<T>(sm.dyl[t * Pt::P + p]);
-                    y[j][i] *= sm.s.e[t];
-                    (i < 2 ? va : vb) += y[j][i] * dy;
+                for (int i = 0; i < 4; i += 2) {
+                    const int at = (i ? rb : ra) * Pt::P + cb + 8 * j;
+                    float dy[2];
+                    load_shared<2>(sm.dyh + at, dy);
+                    if constexpr (!M::kExact32) {
+                        float lo[2];
+                        load_shared<2>(sm.dyl + at, lo);
+                        dy[0] += lo[0], dy[1] += lo[1];
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        y[j][i + n] *= i ? eb : ea;
+                        (i ? vb : va) += y[j][i + n] * dy[n];
+                        x[j][i + n] = fmaf(D, dy[n], x[j][i + n]);
+                    }
                 }
             va = quad_sum(va);
             vb = quad_sum(vb);
             if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
+            store_part(static_cast<T*>(k.du), x);
             if (z) {
                 warp_gemm<T, false, true, 4>(y, sm.m1, Pt::Q, 16 * wr, sm.x, Pt::P, 32 * wc, 0, 16 * wr + 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = i < 2 ? ra : rb, p = cb + 8 * j + (i & 1);
-                        if (t >= rows || p >= a.P) continue;
+                    for (int i = 0; i < 4; i += 2) {
+                        const int t = i ? rb : ra, p = cb + 8 * j;
+                        float uv[2], dv[2] = {0.f, 0.f}, zv[2] = {0.f, 0.f};
+                        load_shared<2>(sm.x + t * Pt::P + p, uv);
                         const int64_t at = ((tok + t) * a.H + h) * a.P + p;
-                        const float yv = fmaf(D, to_f32<T>(sm.x[t * Pt::P + p]), y[j][i]);
-                        static_cast<T*>(k.dz)[at] = from_f32<T>(IO<T>::load(dout, at) * yv * dsilu(IO<T>::load(z, at)));
+                        if (t < rows && p < a.P) {
+                            if (a.vec) {
+                                load_vec<2>(dout + at, dv);
+                                load_vec<2>(z + at, zv);
+                            } else {
+                                dv[0] = IO<T>::load(dout, at), zv[0] = IO<T>::load(z, at);
+                                if (p + 1 < a.P) dv[1] = IO<T>::load(dout, at + 1), zv[1] = IO<T>::load(z, at + 1);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            y[j][i + n] = dv[n] * fmaf(D, uv[n], y[j][i + n]) * dsilu(zv[n]);
                     }
+                store_part(static_cast<T*>(k.dz), y);
             }
         }
         // dC (wc = 0, rows t) or dB (wc = 1, rows s), at most 64 columns n at a time
@@ -350,13 +405,13 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(HeadsBwdArgs k) {
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t >= rows) continue;
-                const float dl = sm.s.dl[t], qv = dl * A;
+                const float dl = sm.steps.dl[t], qv = dl * A;
                 // dq_t is e^q_t R . S, got as a difference of sums that are not small with it; below
                 // q = -20 it is under 2^-28 of R . S, less than those sums' roundings, which a large
                 // step size would magnify
                 const float dq = qv < -20.f ? 0.f : (float)dq2[i];
                 float r = fmaf(dq, A, dw[i] * ex2(qv * kLog2e));
-                if (a.softplus) r *= sigmoid(sm.s.raw[t]);
+                if (a.softplus) r *= sigmoid(sm.steps.raw[t]);
                 sa += fmaf(dq, dl, dw[i] * dl * dl * dw_slope(qv));
                 sb += r;
                 IO<T>::store(static_cast<T*>(k.ddelta), (tok + t) * a.H + h, r);
@@ -504,7 +559,7 @@ extern "C" sscan_status sscan_heads_bwd(const sscan_heads_problem* p, const void
     HeadsBwdArgs k{};
     HeadsArgs& a = k.f;
     a = heads_args(p, u, delta_raw, delta_bias, A, B, C, D_skip, z, h0);
-    a.vec = a.vec && aligned_to(z, 16) && aligned_to(dout, 16);
+    a.vec = a.vec && aligned_to(z, 16) && aligned_to(dout, 16) && aligned_to(du, 16) && aligned_to(dz, 16);
     a.nseg = a.chunks;
     a.seg_chunks = 1;
     a.decays = reinterpret_cast<float*>(ws + l.dec);

@@ -184,6 +184,24 @@ def test_unaligned_pointers(cuda_device, io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["u", "B", "C", "z", "dout", "out"])
+def test_one_unaligned_pointer(cuda_device, io, name):
+    """Wide accesses need every tensor they touch on a 16-byte boundary, not the first one only."""
+    x = case((1, 70, 2, 64, 32, 1), 16, io, cuda_device)
+    dout = randn_like(x["u"], 2)
+    want, grads = sb.sscan_heads_fwd(**x), bwd(x, dout)
+    if name == "dout":
+        dout = R.shifted(dout)
+    elif name != "out":
+        x[name] = R.shifted(x[name])
+    out = R.shifted(torch.empty_like(want)) if name == "out" else None
+    assert torch.equal(sb.sscan_heads_fwd(**x, out=out), want)
+    again = bwd(x, dout)
+    assert all(torch.equal(grads[k], again[k]) for k in grads)
+
+
+@pytest.mark.gpu
 def test_repeats_graphs_and_streams(cuda_device):
     x = case((2, 3000, 4, 32, 32, 2), 9, "bf16", cuda_device)
     dout = randn_like(x["u"], 5)
