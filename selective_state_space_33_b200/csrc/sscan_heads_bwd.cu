@@ -86,6 +86,8 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Loads a P x N fp32 state into two tiles of T ([p][n], zero-padded).
 template <typename T, int NT, typename Each>
 __device__ __forceinline__ void load_state(T* hi, T* lo, const float* src, int P, int N, int tid, Each each) {
@@ -192,6 +194,20 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                     if (i == tid + j * kThreads)
                         for (int e = 0; e < 4; ++e) ssum = fmaf(sv[j][e], v[e], ssum);
             });
+        }
+        // the next head's tiles on their way to L2 while this one is worked on
+        if (h + 1 < h_end) {
+            if (tid < kQ && tid < rows) {
+                const int64_t at = ((tok + tid) * a.H + h + 1) * a.P;
+                prefetch_l2(u + at);
+                prefetch_l2(dout + at);
+                if (z) prefetch_l2(z + at);
+            }
+            const int64_t at = ((bh + 1) * a.chunks + c) * a.P * a.N;
+            for (int i = tid * 32; i < a.P * a.N; i += kThreads * 32) {
+                prefetch_l2(a.states + at + i);
+                prefetch_l2(k.R + at + i);
+            }
         }
         dsum = warp_sum(dsum);
         ssum = warp_sum(ssum);
@@ -329,27 +345,41 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
             store_part(static_cast<T*>(k.du), x);
             if (z) {
+                // dout and z again, in this warp's layout, ahead of the product that hides their latency
+                Vec<T, 2> dv[4][2], zv[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = i ? rb : ra, p = cb + 8 * j;
+                        const int64_t at = ((tok + t) * a.H + h) * a.P + p;
+                        dv[j][i].zero();
+                        zv[j][i].zero();
+                        if (t < rows && p < a.P) {
+                            if (a.vec) {
+                                dv[j][i].load(dout + at);
+                                zv[j][i].load(z + at);
+                            } else {
+                                const bool two = p + 1 < a.P;
+                                const float d2[2] = {IO<T>::load(dout, at), two ? IO<T>::load(dout, at + 1) : 0.f};
+                                const float z2[2] = {IO<T>::load(z, at), two ? IO<T>::load(z, at + 1) : 0.f};
+                                dv[j][i].set(d2);
+                                zv[j][i].set(z2);
+                            }
+                        }
+                    }
                 warp_gemm<T, false, true, 4>(y, sm.m1, Pt::Q, 16 * wr, sm.x, Pt::P, 32 * wc, 0, 16 * wr + 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const int t = i ? rb : ra, p = cb + 8 * j;
-                        float uv[2], dv[2] = {0.f, 0.f}, zv[2] = {0.f, 0.f};
-                        load_shared<2>(sm.x + t * Pt::P + p, uv);
-                        const int64_t at = ((tok + t) * a.H + h) * a.P + p;
-                        if (t < rows && p < a.P) {
-                            if (a.vec) {
-                                load_vec<2>(dout + at, dv);
-                                load_vec<2>(z + at, zv);
-                            } else {
-                                dv[0] = IO<T>::load(dout, at), zv[0] = IO<T>::load(z, at);
-                                if (p + 1 < a.P) dv[1] = IO<T>::load(dout, at + 1), zv[1] = IO<T>::load(z, at + 1);
-                            }
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        float uv[2], d2[2], z2[2];
+                        load_shared<2>(sm.x + (i ? rb : ra) * Pt::P + cb + 8 * j, uv);
+                        dv[j][i].get(d2);
+                        zv[j][i].get(z2);
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
-                            y[j][i + n] = dv[n] * fmaf(D, uv[n], y[j][i + n]) * dsilu(zv[n]);
+                            y[j][2 * i + n] = d2[n] * fmaf(D, uv[n], y[j][2 * i + n]) * dsilu(z2[n]);
                     }
                 store_part(static_cast<T*>(k.dz), y);
             }
