@@ -93,8 +93,9 @@ __device__ __forceinline__ void chunk_outputs(float (&y)[PTL][4], const T* C, co
         y[j][2] *= eb, y[j][3] *= eb;
     }
     const float cha = sc.ch[ta], cla = sc.cl[ta], chb = sc.ch[tb], clb = sc.cl[tb];
+    typename M::Addr x_at = M::at_bt(x, PP, p0);
 #pragma unroll 1
-    for (int s0 = 0; s0 <= t0; s0 += 16) {
+    for (int s0 = 0; s0 <= t0; s0 += 16, x_at += M::template step_k<true>(PP) * (16 / M::KS)) {
         float m[2][4];
         zero_acc(m);
         warp_gemm<T, false, false, 2>(m, C, PN, t0, B, PN, s0, 0, NT);
@@ -116,7 +117,7 @@ __device__ __forceinline__ void chunk_outputs(float (&y)[PTL][4], const T* C, co
 #pragma unroll
             for (int j = 0; j < PTL; j += 2) {
                 typename M::B b0, b1;
-                M::load_bt2(b0, b1, x, PP, p0 + 8 * j, s0 + 8 * k);
+                M::template fetch_b2<true>(b0, b1, x_at + M::template step_k<true>(PP) * (k / M::KT) + M::template step_n<true>(PP) * (j / 2), PP);
                 if constexpr (FINITE) M::keep_finite(b0), M::keep_finite(b1);
                 M::mma(y[j], fa, b0);
                 M::mma(y[j + 1], fa, b1);
@@ -313,13 +314,13 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
 #pragma unroll
             for (int k = 0; k < kQ; k += M::KS) {
                 typename M::A fa;
-                M::load_at(fa, t.x, PP, p0, k);
+                M::template fetch_a<true>(fa, M::at_at(t.x, PP, p0) + M::template step_k<true>(PP) * (k / M::KS), PP);
 #pragma unroll
                 for (int part = 2; part >= 0; --part)
 #pragma unroll
                     for (int j = 0; j < NTL; j += 2) {
                         typename M::B b0, b1;
-                        M::load_bt2(b0, b1, sm.fb[part], NT, n0 + 8 * j, k);
+                        M::template fetch_b2<true>(b0, b1, M::at_bt(sm.fb[part], NT, n0) + M::template step_k<true>(NT) * (k / M::KS) + M::template step_n<true>(NT) * (j / 2), NT);
                         M::mma(part ? lo[j] : hi[j], fa, b0);
                         M::mma(part ? lo[j + 1] : hi[j + 1], fa, b1);
                     }
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
 #pragma unroll
                 for (int j = 0; j < NTL; j += 2) {
                     typename M::B b0, b1;
-                    M::load_bt2(b0, b1, t.B, PN, n0 + 8 * j, k);
+                    M::template fetch_b2<true>(b0, b1, M::at_bt(t.B, PN, n0) + M::template step_k<true>(PN) * (k / M::KS) + M::template step_n<true>(PN) * (j / 2), PN);
                     mma_split(hi[j], lo[j], fa, b0);
                     mma_split(hi[j + 1], lo[j + 1], fa, b1);
                 }

@@ -254,10 +254,13 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                 warp_gemm<T, false, false, 4>(Hm, sm.dyl, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
         }
         float rowa = 0.f, rowb = 0.f;
+        const float cha = sm.s.ch[ra], cla = sm.s.cl[ra], chb = sm.s.ch[rb], clb = sm.s.cl[rb];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int s0 = cb + 8 * j;
             const float2 ws = *reinterpret_cast<const float2*>(sm.s.w + s0);
+            const float2 chs = *reinterpret_cast<const float2*>(sm.s.ch + s0);
+            const float2 cls = *reinterpret_cast<const float2*>(sm.s.cl + s0);
             float cols[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
@@ -265,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                 float m1[2], m2[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float E = chunk_decay(sm.s, t, s0 + n), w_ = n ? ws.y : ws.x;
+                    const float E = ex2(((i ? chb : cha) - (n ? chs.y : chs.x)) + ((i ? clb : cla) - (n ? cls.y : cls.x)));
+                    const float w_ = n ? ws.y : ws.x;
                     const bool in = s0 + n <= t;
                     const float ge = in ? G[j][i + n] * E : 0.f, he = in ? Hm[j][i + n] * E : 0.f;
                     const float pair = in ? ge * Hm[j][i + n] : 0.f;

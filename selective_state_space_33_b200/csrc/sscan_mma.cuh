@@ -27,36 +27,46 @@ template <> struct Mma<__nv_bfloat16> {
     struct A { uint32_t r[4]; };
     struct B { uint32_t r[2]; };
 
-    static __device__ __forceinline__ uint32_t addr(const T* p) {
+    // Where a lane's ldmatrix row starts, for k = 0: the four ways an operand can be stored, as
+    // shared-memory byte addresses, and how far k .. k + 15 and the next 16 columns are from there.
+    using Addr = uint32_t;
+    static __device__ __forceinline__ Addr addr(const T* p) {
         return static_cast<uint32_t>(__cvta_generic_to_shared(p));
     }
-    // rows m0 .. m0+15, k0 .. k0+15 of a tile stored [m][k]
-    static __device__ __forceinline__ void load_a(A& a, const T* s, int pitch, int m0, int k0) {
+    static __device__ __forceinline__ Addr at_a(const T* s, int pitch, int m0) {   // [m][k]
         const int l = threadIdx.x & 31;
-        const uint32_t p = addr(s + (m0 + (l & 15)) * pitch + k0 + (l >> 4) * 8);
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(a.r[0]), "=r"(a.r[1]), "=r"(a.r[2]), "=r"(a.r[3]) : "r"(p) : "memory");
+        return addr(s + (m0 + (l & 15)) * pitch + (l >> 4) * 8);
     }
-    // the same from a tile stored [k][m]
-    static __device__ __forceinline__ void load_at(A& a, const T* s, int pitch, int m0, int k0) {
+    static __device__ __forceinline__ Addr at_at(const T* s, int pitch, int m0) {  // [k][m]
         const int l = threadIdx.x & 31;
-        const uint32_t p = addr(s + (k0 + (l & 7) + (l >> 4) * 8) * pitch + m0 + ((l >> 3) & 1) * 8);
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(a.r[0]), "=r"(a.r[1]), "=r"(a.r[2]), "=r"(a.r[3]) : "r"(p) : "memory");
+        return addr(s + ((l & 7) + (l >> 4) * 8) * pitch + m0 + ((l >> 3) & 1) * 8);
     }
-    // columns n0 .. n0+15 (two fragments), k0 .. k0+15 of a tile stored [n][k]
-    static __device__ __forceinline__ void load_b2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+    static __device__ __forceinline__ Addr at_b(const T* s, int pitch, int n0) {   // [n][k]
         const int l = threadIdx.x & 31;
-        const uint32_t p = addr(s + (n0 + (l & 7) + (l >> 4) * 8) * pitch + k0 + ((l >> 3) & 1) * 8);
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(b0.r[0]), "=r"(b0.r[1]), "=r"(b1.r[0]), "=r"(b1.r[1]) : "r"(p) : "memory");
+        return addr(s + (n0 + (l & 7) + (l >> 4) * 8) * pitch + ((l >> 3) & 1) * 8);
     }
-    // the same from a tile stored [k][n]
-    static __device__ __forceinline__ void load_bt2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
+    static __device__ __forceinline__ Addr at_bt(const T* s, int pitch, int n0) {  // [k][n]
         const int l = threadIdx.x & 31;
-        const uint32_t p = addr(s + (k0 + (l & 15)) * pitch + n0 + (l >> 4) * 8);
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(b0.r[0]), "=r"(b0.r[1]), "=r"(b1.r[0]), "=r"(b1.r[1]) : "r"(p) : "memory");
+        return addr(s + (l & 15) * pitch + n0 + (l >> 4) * 8);
+    }
+    template <bool TR> static __device__ __forceinline__ Addr step_k(int pitch) { return TR ? 16 * pitch * 2 : 32; }
+    template <bool TR> static __device__ __forceinline__ Addr step_n(int pitch) { return TR ? 32 : 16 * pitch * 2; }
+
+    template <bool TR> static __device__ __forceinline__ void load4(uint32_t (&r)[4], Addr p) {
+        if constexpr (TR)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+        else
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+    }
+    // 16 rows by 16 k
+    template <bool TR> static __device__ __forceinline__ void fetch_a(A& a, Addr p, int) { load4<TR>(a.r, p); }
+    // 16 k by 16 columns: two fragments
+    template <bool TR> static __device__ __forceinline__ void fetch_b2(B& b0, B& b1, Addr p, int) {
+        uint32_t r[4];
+        load4<TR>(r, p);
+        b0.r[0] = r[0], b0.r[1] = r[1], b1.r[0] = r[2], b1.r[1] = r[3];
     }
     // infinities and NaN (all exponent bits set) become 0
     static __device__ __forceinline__ void keep_finite(B& b) {
@@ -99,41 +109,31 @@ template <> struct Mma<float> {
         asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
     }
     static __device__ __forceinline__ void put(A& a, int i, float x) { split(x, a.hi[i], a.lo[i]); }
-    static __device__ __forceinline__ void load_a(A& a, const T* s, int pitch, int m0, int k0) {
-        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-        const float* p = s + (m0 + g) * pitch + k0 + 2 * t;
+    // A lane's first element, for k = 0, as a pointer; the steps are in elements.
+    using Addr = const float*;
+    static __device__ __forceinline__ Addr at_a(const T* s, int pitch, int m0) {
+        return s + (m0 + ((threadIdx.x & 31) >> 2)) * pitch + 2 * (threadIdx.x & 3);
+    }
+    static __device__ __forceinline__ Addr at_at(const T* s, int pitch, int m0) {
+        return s + 2 * (threadIdx.x & 3) * pitch + m0 + ((threadIdx.x & 31) >> 2);
+    }
+    static __device__ __forceinline__ Addr at_b(const T* s, int pitch, int n0) { return at_a(s, pitch, n0); }
+    static __device__ __forceinline__ Addr at_bt(const T* s, int pitch, int n0) { return at_at(s, pitch, n0); }
+    template <bool TR> static __device__ __forceinline__ int step_k(int pitch) { return TR ? 8 * pitch : 8; }
+    template <bool TR> static __device__ __forceinline__ int step_n(int pitch) { return TR ? 16 : 16 * pitch; }
+    template <bool TR> static __device__ __forceinline__ void fetch_a(A& a, Addr p, int pitch) {
+        const int m = TR ? 8 : 8 * pitch, k = TR ? pitch : 1;  // 8 rows on, one k on
         put(a, 0, p[0]);
-        put(a, 1, p[8 * pitch]);
-        put(a, 2, p[1]);
-        put(a, 3, p[8 * pitch + 1]);
+        put(a, 1, p[m]);
+        put(a, 2, p[k]);
+        put(a, 3, p[m + k]);
     }
-    static __device__ __forceinline__ void load_at(A& a, const T* s, int pitch, int m0, int k0) {
-        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-        const float* p = s + (k0 + 2 * t) * pitch + m0 + g;
-        put(a, 0, p[0]);
-        put(a, 1, p[8]);
-        put(a, 2, p[pitch]);
-        put(a, 3, p[pitch + 8]);
-    }
-    static __device__ __forceinline__ void load_b(B& b, const T* s, int pitch, int n0, int k0) {
-        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-        const float* p = s + (n0 + g) * pitch + k0 + 2 * t;
-        split(p[0], b.hi[0], b.lo[0]);
-        split(p[1], b.hi[1], b.lo[1]);
-    }
-    static __device__ __forceinline__ void load_bt(B& b, const T* s, int pitch, int n0, int k0) {
-        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-        const float* p = s + (k0 + 2 * t) * pitch + n0 + g;
-        split(p[0], b.hi[0], b.lo[0]);
-        split(p[pitch], b.hi[1], b.lo[1]);
-    }
-    static __device__ __forceinline__ void load_b2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
-        load_b(b0, s, pitch, n0, k0);
-        load_b(b1, s, pitch, n0 + 8, k0);
-    }
-    static __device__ __forceinline__ void load_bt2(B& b0, B& b1, const T* s, int pitch, int n0, int k0) {
-        load_bt(b0, s, pitch, n0, k0);
-        load_bt(b1, s, pitch, n0 + 8, k0);
+    template <bool TR> static __device__ __forceinline__ void fetch_b2(B& b0, B& b1, Addr p, int pitch) {
+        const int n = TR ? 8 : 8 * pitch, k = TR ? pitch : 1;
+        split(p[0], b0.hi[0], b0.lo[0]);
+        split(p[k], b0.hi[1], b0.lo[1]);
+        split(p[n], b1.hi[0], b1.lo[0]);
+        split(p[n + k], b1.hi[1], b1.lo[1]);
     }
     static __device__ __forceinline__ void keep_finite(B& b) {
 #pragma unroll
@@ -158,25 +158,29 @@ template <> struct Mma<float> {
     }
 };
 
-// acc[NTL][4] (16 rows m0.. by 8 NTL columns n0..) += A[m][k] B[k][n], k = 0 .. K-1.
+// acc[NTL][4] (16 rows m0.. by 8 NTL columns n0..) += A[m][k] B[k][n], k = k_begin .. k_end - 1.
 // AT / BT: the operand's tile is stored [k][m] / [k][n] instead of [m][k] / [n][k].  NTL is even.
 template <typename T, bool AT, bool BT, int NTL>
 __device__ __forceinline__ void warp_gemm(float (&acc)[NTL][4], const T* A, int pa, int m0, const T* B, int pb, int n0,
                                           int k_begin, int k_end) {
     using M = Mma<T>;
-#pragma unroll 2
+    typename M::Addr a_at = AT ? M::at_at(A, pa, m0) : M::at_a(A, pa, m0);
+    typename M::Addr b_at = BT ? M::at_bt(B, pb, n0) : M::at_b(B, pb, n0);
+    a_at += M::template step_k<AT>(pa) * (k_begin / M::KS);
+    b_at += M::template step_k<BT>(pb) * (k_begin / M::KS);
+#pragma unroll 4
     for (int k = k_begin; k < k_end; k += M::KS) {
         typename M::A a;
-        if constexpr (AT) M::load_at(a, A, pa, m0, k);
-        else M::load_a(a, A, pa, m0, k);
+        M::template fetch_a<AT>(a, a_at, pa);
 #pragma unroll
         for (int j = 0; j < NTL; j += 2) {
             typename M::B b0, b1;
-            if constexpr (BT) M::load_bt2(b0, b1, B, pb, n0 + 8 * j, k);
-            else M::load_b2(b0, b1, B, pb, n0 + 8 * j, k);
+            M::template fetch_b2<BT>(b0, b1, b_at + M::template step_n<BT>(pb) * (j / 2), pb);
             M::mma(acc[j], a, b0);
             M::mma(acc[j + 1], a, b1);
         }
+        a_at += M::template step_k<AT>(pa);
+        b_at += M::template step_k<BT>(pb);
     }
 }
 
@@ -207,7 +211,7 @@ template <typename Fn>
 __device__ __forceinline__ void load_at_split(Split<__nv_bfloat16>& a, const __nv_bfloat16* s, int pitch, int m0, int k0,
                                               Fn fn) {
     Mma<__nv_bfloat16>::A raw;
-    Mma<__nv_bfloat16>::load_at(raw, s, pitch, m0, k0);
+    Mma<__nv_bfloat16>::fetch_a<true>(raw, Mma<__nv_bfloat16>::at_at(s + k0 * pitch, pitch, m0), pitch);
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
