@@ -30,9 +30,12 @@ struct Walk {
     static constexpr int WC = NT == 128 ? 2 : 1;
     static constexpr int NW = 4 * WC, threads = 32 * (NW + 1);
     // blocks per SM that shared memory allows, and registers are held to
-    static constexpr int blocks = NT <= 32 ? 3 : bf16 || NT == 64 ? 2 : 1;
-    // two buffers of tiles where three blocks or more still fit an SM
-    static constexpr int stages = bf16 && NT <= 64 ? 2 : 1;
+    static constexpr int blocks = NT <= 32 ? 3 : NT == 64 ? (bf16 ? 3 : 2) : bf16 ? 2 : 1;
+    static constexpr int stages = bf16 ? 2 : 1;  // buffers of tiles
+    // From 64 states on, the state goes into the outputs as one bf16 part (its rounding is then the
+    // same size as that of M on the other terms), the gate waits in registers, and the outputs
+    // are staged in the rows of C that their own warps alone read: more blocks fit an SM.
+    static constexpr bool big = bf16 && NT >= 64;
     // up to 32 states B is the smaller factor to scale, once per block through shared memory;
     // above, each warp scales its own 16 channels of u in registers
     static constexpr bool scale_b = bf16 && out && NT <= 32;
@@ -48,7 +51,7 @@ struct Walk {
         Tiles t[stages];
         alignas(16) T z[out ? kQ * PITCH_P : 8];             // the gate, then the outputs
         alignas(16) T sh[out ? kHeadDim * PITCH_N : 8];      // the state, [p][n]
-        alignas(16) T sl[out && bf16 ? kHeadDim * PITCH_N : 8];
+        alignas(16) T sl[out && bf16 && !big ? kHeadDim * PITCH_N : 8];
         alignas(16) T fb[scale_b ? 3 : 1][scale_b ? kQ * NT : 8];  // f B in three parts
         ChunkScalars s[2];
     };
@@ -85,7 +88,7 @@ __device__ __forceinline__ void chunk_outputs(float (&y)[PTL][4], const T* C, co
     const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3, ta = t0 + g, tb = ta + 8;
     zero_acc(y);
     warp_gemm<T, false, false, PTL>(y, C, PN, t0, sh, PN, p0, 0, NT);
-    if constexpr (!M::kExact32) warp_gemm<T, false, false, PTL>(y, C, PN, t0, sl, PN, p0, 0, NT);
+    if constexpr (!M::kExact32 && NT < 64) warp_gemm<T, false, false, PTL>(y, C, PN, t0, sl, PN, p0, 0, NT);
     const float ea = sc.e[ta], eb = sc.e[tb];
 #pragma unroll
     for (int j = 0; j < PTL; ++j) {
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
         const ChunkScalars& sc = sm.s[i & 1];
         if constexpr (W::out) {
             // the gate: a warp's own 16 steps (and, with two warps on them, both halves)
-            if (z)
+            if (z && !W::big)
                 load_rows_async<T>(sm.z + p0 * PP, PP, z + (row + (int64_t)p0 * a.H) * a.P, (int64_t)a.H * a.P, rows - p0,
                                    a.P, a.vec);
             cp_async_commit();
@@ -224,7 +227,8 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                 for (int k = 0; k < 2; ++k) {
                     const int at = (p0 + g + 8 * k) * PN + n0 + 8 * j + 2 * q;
                     const float x = S[j][2 * k], y = S[j][2 * k + 1];
-                    split_store2<T>(sm.sh, sm.sl, at, x, y);
+                    if constexpr (W::big) *reinterpret_cast<uint32_t*>(sm.sh + at) = M::pack(x, y);
+                    else split_store2<T>(sm.sh, sm.sl, at, x, y);
                 }
             if constexpr (W::scale_b) {
 #pragma unroll
@@ -246,6 +250,25 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             float y[PTL][4];
             const int c_p = kHeadDim / WC * wc;
             const int ta = p0 + g, tb = ta + 8;              // the rows of y are steps
+            Vec<T, 2> zr[W::big ? PTL : 1][2];
+            if (W::big && z) {
+#pragma unroll
+                for (int j = 0; j < PTL; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int st = k ? tb : ta, p = c_p + 8 * j + 2 * q;
+                        const int64_t at = (row + (int64_t)st * a.H) * a.P + p;
+                        zr[j][k].zero();
+                        if (st < rows && p < a.P) {
+                            if (a.vec) {
+                                zr[j][k].load(z + at);
+                            } else {
+                                const float two[2] = {IO<T>::load(z, at), p + 1 < a.P ? IO<T>::load(z, at + 1) : 0.f};
+                                zr[j][k].set(two);
+                            }
+                        }
+                    }
+            }
             const T* sl = W::bf16 ? sm.sl : nullptr;
             chunk_outputs<T, NT, PTL, false>(y, t.C, t.B, t.x, sm.sh, sl, sc, p0, c_p);
             // A value of u that is not finite meets the zeros of M above the diagonal in the product.
@@ -265,26 +288,31 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                         y[j][k] += not_finite_terms(t.C, t.B, t.x, sc, PN, PP, a.N, k < 2 ? ta : tb,
                                                     c_p + 8 * j + 2 * q + (k & 1));
             }
-            // skip term and gate, through the gate's own rows of shared memory to 16-byte stores
-            if (W::stages == 2) cp_async_wait<1>();
-            else cp_async_wait<0>();
+            // skip term and gate, through rows of shared memory to 16-byte stores
+            if (!W::big) {
+                if (W::stages == 2) cp_async_wait<1>();
+                else cp_async_wait<0>();
+            }
             if (WC > 1) product_sync<kWork>();
             else __syncwarp();
+            T* stage = W::big ? t.C : sm.z;
+            constexpr int PS = W::big ? PN : PP;
             const float D = a.D ? __ldg(a.D + h) : 0.f;
 #pragma unroll
             for (int j = 0; j < PTL; ++j)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int at = (k ? tb : ta) * PP + c_p + 8 * j + 2 * q;
+                    const int st = k ? tb : ta, p = c_p + 8 * j + 2 * q;
                     float xv[2], v[2] = {y[j][2 * k], y[j][2 * k + 1]};
-                    load_shared<2>(t.x + at, xv);
+                    load_shared<2>(t.x + st * PP + p, xv);
                     if (a.D) v[0] = fmaf(D, xv[0], v[0]), v[1] = fmaf(D, xv[1], v[1]);
                     if (z) {
                         float zv[2];
-                        load_shared<2>(sm.z + at, zv);
+                        if constexpr (W::big) zr[j][k].get(zv);
+                        else load_shared<2>(sm.z + st * PP + p, zv);
                         v[0] *= silu(zv[0]), v[1] *= silu(zv[1]);
                     }
-                    store_vec<2>(sm.z + at, v);
+                    store_vec<2>(stage + st * PS + p, v);
                 }
             __syncwarp();
             constexpr int VE = 16 / sizeof(T), PER = kHeadDim / WC / VE;
@@ -295,11 +323,11 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                 if (st >= rows || p >= a.P) continue;
                 const int64_t at = (row + (int64_t)st * a.H) * a.P + p;
                 if (a.vec) {
-                    *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(sm.z + st * PP + p);
+                    *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(stage + st * PS + p);
                 } else {
 #pragma unroll
                     for (int v = 0; v < VE; ++v)
-                        if (p + v < a.P) out[at + v] = sm.z[st * PP + p + v];
+                        if (p + v < a.P) out[at + v] = stage[st * PS + p + v];
                 }
             }
         }
@@ -307,9 +335,8 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
         // S' = exp(c_end) S + (f U)^T B
         const float dec = ex2(sc.total * kLog2e);
         total += sc.total;
-        float hi[NTL][4], lo[NTL][4];
-        zero_acc(hi);
-        zero_acc(lo);
+        float acc[NTL][4];
+        zero_acc(acc);
         if constexpr (W::scale_b) {
 #pragma unroll
             for (int k = 0; k < kQ; k += M::KS) {
@@ -321,13 +348,16 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                     for (int j = 0; j < NTL; j += 2) {
                         typename M::B b0, b1;
                         M::template fetch_b2<true>(b0, b1, M::at_bt(sm.fb[part], NT, n0) + M::template step_k<true>(NT) * (k / M::KS) + M::template step_n<true>(NT) * (j / 2), NT);
-                        M::mma(part ? lo[j] : hi[j], fa, b0);
-                        M::mma(part ? lo[j + 1] : hi[j + 1], fa, b1);
+                        M::mma(acc[j], fa, b0);
+                        M::mma(acc[j + 1], fa, b1);
                     }
             }
         } else {
+            float lo[W::bf16 ? 1 : NTL][4];
+            zero_acc(lo);
+            typename M::Addr b_at = M::at_bt(t.B, PN, n0);
 #pragma unroll 1
-            for (int k = 0; k < kQ; k += M::KS) {
+            for (int k = 0; k < kQ; k += M::KS, b_at += M::template step_k<true>(PN)) {
                 Split<T> fa;
                 load_at_split(fa, t.x, PP, p0, k, [&](float v, int p, int s) {
                     if (!kRev) return v * sc.f[s];
@@ -336,16 +366,27 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
 #pragma unroll
                 for (int j = 0; j < NTL; j += 2) {
                     typename M::B b0, b1;
-                    M::template fetch_b2<true>(b0, b1, M::at_bt(t.B, PN, n0) + M::template step_k<true>(PN) * (k / M::KS) + M::template step_n<true>(PN) * (j / 2), PN);
-                    mma_split(hi[j], lo[j], fa, b0);
-                    mma_split(hi[j + 1], lo[j + 1], fa, b1);
+                    M::template fetch_b2<true>(b0, b1, b_at + M::template step_n<true>(PN) * (j / 2), PN);
+                    if constexpr (W::bf16) {
+                        mma_split(acc[j], fa, b0);
+                        mma_split(acc[j + 1], fa, b1);
+                    } else {
+                        mma_split(acc[j], lo[j], fa, b0);
+                        mma_split(acc[j + 1], lo[j + 1], fa, b1);
+                    }
                 }
+            }
+            if constexpr (!W::bf16) {
+#pragma unroll
+                for (int j = 0; j < NTL; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[j][k] += lo[j][k];
             }
         }
 #pragma unroll
         for (int j = 0; j < NTL; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) S[j][k] = fmaf(dec, S[j][k], hi[j][k] + lo[j][k]);
+            for (int k = 0; k < 4; ++k) S[j][k] = fmaf(dec, S[j][k], acc[j][k]);
     }
     if (MODE == kWalkOut) {
         if (a.h_last && seg == a.nseg - 1) {
@@ -519,13 +560,25 @@ void launch_step_heads(const HeadsArgs& a, float* state, cudaStream_t st) {
     }
 }
 
-// Segments of a forward pass: one block per (batch, head) where those fill the GPU, else
-// enough segments for about four blocks per SM, of at least four chunks.
-void plan_heads(HeadsArgs& a) {
+// Blocks of the output kernel that the GPU holds at once.
+int64_t heads_slots(const HeadsArgs& a, bool bf16) {
+    auto per = [&](auto t) {
+        using T = decltype(t);
+        return a.N <= 16 ? Walk<T, 16, kWalkOut>::blocks : a.N <= 32 ? Walk<T, 32, kWalkOut>::blocks
+               : a.N <= 64 ? Walk<T, 64, kWalkOut>::blocks : Walk<T, 128, kWalkOut>::blocks;
+    };
+    return 148 * (int64_t)(bf16 ? per(__nv_bfloat16{}) : per(float{}));
+}
+
+// Segments of a forward pass.  With fewer (batch, head) pairs than SMs a sequence is split into as
+// many segments, of at least four chunks, as fill the GPU once: a block more than it holds would
+// wait for a whole segment (65536 steps, 24 heads, 128 states: 25 segments, 600 blocks where 296
+// fit, 1750 us; 12 segments, 288 blocks, 1190 us).
+void plan_heads(HeadsArgs& a, bool bf16) {
     const int64_t bh = a.batch * a.H;
     int64_t nseg = 1;
-    if (bh < 3 * 148) {
-        nseg = (4 * 148 + bh - 1) / bh;
+    if (bh < 148) {
+        nseg = heads_slots(a, bf16) / bh;
         if (nseg > (a.chunks + 3) / 4) nseg = (a.chunks + 3) / 4;
         if (nseg < 2) nseg = 1;
     }
@@ -597,7 +650,7 @@ void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, fl
 
 size_t heads_fwd_bytes(const sscan_heads_problem* p) {
     HeadsArgs a = heads_args(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-    plan_heads(a);
+    plan_heads(a, p->io_dtype == SSCAN_BF16);
     return a.nseg > 1 ? split_bytes(a) : 0;
 }
 
@@ -637,8 +690,8 @@ sscan_status sscan_heads_fwd(const sscan_heads_problem* p, const void* u, const 
     HeadsArgs a = heads_args(p, u, delta_raw, delta_bias, A, B, C, D_skip, z, h0);
     a.out = out, a.h_last = h_last;
     a.vec = a.vec && aligned_to(z, 16) && aligned_to(out, 16);
-    plan_heads(a);
     const bool bf16 = p->io_dtype == SSCAN_BF16;
+    plan_heads(a, bf16);
     cudaError_t e = cudaSuccess;
     if (a.nseg > 1) {
         a.states = static_cast<float*>(workspace);

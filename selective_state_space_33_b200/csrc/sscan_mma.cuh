@@ -229,19 +229,18 @@ __device__ __forceinline__ void load_at_split(Split<float>& a, const float* s, i
     Mma<float>::put(a.part[0], 3, fn(p[pitch + 8], m0 + g + 8, k0 + 2 * t + 1));
 }
 
-// Products with the leading parts go to `hi`, the corrections to `lo`: the tensor core's
-// accumulation drops low bits at each step, so the small terms are kept apart, the large
-// ones take fewer steps, and the caller adds the two in fp32.
-__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const Split<__nv_bfloat16>& a,
-                                          const Mma<__nv_bfloat16>::B& b) {
-    Mma<__nv_bfloat16>::mma(lo, a.part[2], b);
-    Mma<__nv_bfloat16>::mma(lo, a.part[1], b);
-    Mma<__nv_bfloat16>::mma(hi, a.part[0], b);
+// acc += a b with every part of a, the small ones first.
+__device__ __forceinline__ void mma_split(float (&acc)[4], const Split<__nv_bfloat16>& a, const Mma<__nv_bfloat16>::B& b) {
+#pragma unroll
+    for (int p = 2; p >= 0; --p) Mma<__nv_bfloat16>::mma(acc, a.part[p], b);
 }
-__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const Split<float>& a, const Mma<float>::B& b) {
+// fp32: products with the leading parts go to `acc`, the corrections to `lo`.  The tensor core's
+// accumulation drops low bits at each step, so the small terms are kept apart, the large ones take a
+// third of the steps, and the caller adds the two in fp32.
+__device__ __forceinline__ void mma_split(float (&acc)[4], float (&lo)[4], const Split<float>& a, const Mma<float>::B& b) {
     Mma<float>::one(lo, a.part[0].lo, b.hi);
     Mma<float>::one(lo, a.part[0].hi, b.lo);
-    Mma<float>::one(hi, a.part[0].hi, b.hi);
+    Mma<float>::one(acc, a.part[0].hi, b.hi);
 }
 
 // 16 bytes from global to shared memory, asynchronously; zeros when !in (src is then not read).
