@@ -574,16 +574,24 @@ int64_t heads_slots(const HeadsArgs& a, bool bf16) {
 // many segments, of at least four chunks, as fill the GPU once: a block more than it holds would
 // wait for a whole segment (65536 steps, 24 heads, 128 states: 25 segments, 600 blocks where 296
 // fit, 1750 us; 12 segments, 288 blocks, 1190 us).
-void plan_heads(HeadsArgs& a, bool bf16) {
+void plan_segments(HeadsArgs& a, int64_t slots, int64_t least) {
     const int64_t bh = a.batch * a.H;
     int64_t nseg = 1;
     if (bh < 148) {
-        nseg = heads_slots(a, bf16) / bh;
-        if (nseg > (a.chunks + 3) / 4) nseg = (a.chunks + 3) / 4;
+        nseg = slots / bh;
+        if (nseg > (a.chunks + least - 1) / least) nseg = (a.chunks + least - 1) / least;
         if (nseg < 2) nseg = 1;
     }
     a.seg_chunks = (a.chunks + nseg - 1) / nseg;
     a.nseg = (a.chunks + a.seg_chunks - 1) / a.seg_chunks;
+}
+
+// Whether the tcgen05 kernel takes this problem, pointers (a.vec) aside, and its plan: one block per SM.
+bool tc_problem(const HeadsArgs& a, bool bf16) { return bf16 && a.N > 32 && a.L < (int64_t(1) << 31) - kTcQ; }
+
+void plan_heads(HeadsArgs& a, bool bf16, bool tc) {
+    if (tc) a.chunks = (a.L + kTcQ - 1) / kTcQ;
+    plan_segments(a, tc ? 148 : heads_slots(a, bf16), tc ? 2 : 4);
 }
 
 size_t split_bytes(const HeadsArgs& a) {
@@ -650,8 +658,15 @@ void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, fl
 
 size_t heads_fwd_bytes(const sscan_heads_problem* p) {
     HeadsArgs a = heads_args(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
-    plan_heads(a, p->io_dtype == SSCAN_BF16);
-    return a.nseg > 1 ? split_bytes(a) : 0;
+    const bool bf16 = p->io_dtype == SSCAN_BF16;
+    HeadsArgs t = a;  // either kernel may take the call, by its pointers
+    plan_heads(a, bf16, false);
+    size_t bytes = a.nseg > 1 ? split_bytes(a) : 0;
+    if (tc_problem(t, bf16)) {
+        plan_heads(t, bf16, true);
+        if (t.nseg > 1 && split_bytes(t) > bytes) bytes = split_bytes(t);
+    }
+    return bytes;
 }
 
 size_t heads_bwd_bytes(const sscan_heads_problem* p);
@@ -691,18 +706,20 @@ sscan_status sscan_heads_fwd(const sscan_heads_problem* p, const void* u, const 
     a.out = out, a.h_last = h_last;
     a.vec = a.vec && aligned_to(z, 16) && aligned_to(out, 16);
     const bool bf16 = p->io_dtype == SSCAN_BF16;
-    plan_heads(a, bf16);
+    const bool tc = a.vec && tc_problem(a, bf16);
+    plan_heads(a, bf16, tc);
     cudaError_t e = cudaSuccess;
     if (a.nseg > 1) {
         a.states = static_cast<float*>(workspace);
         a.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                             round256((size_t)(a.batch * a.H * a.nseg * a.P * a.N) * sizeof(float)));
-        e = launch_heads_local(a, nullptr, bf16, st);
+        e = tc ? launch_heads_tc(a, true, st) : launch_heads_local(a, nullptr, bf16, st);
         if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "segment state kernel: %s", cudaGetErrorString(e));
         launch_heads_carry(a, false, h0, nullptr, st);
         if (sscan_status s = api_launched("segment carry kernel")) return s;
     }
-    e = bf16 ? walk_n<__nv_bfloat16, kWalkOut>(a, nullptr, st) : walk_n<float, kWalkOut>(a, nullptr, st);
+    e = tc ? launch_heads_tc(a, false, st)
+        : bf16 ? walk_n<__nv_bfloat16, kWalkOut>(a, nullptr, st) : walk_n<float, kWalkOut>(a, nullptr, st);
     if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "heads forward kernel: %s", cudaGetErrorString(e));
     return SSCAN_OK;
 }

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "sscan_host.h"
+#include "sscan_launch.h"
 #include "sscan_math.cuh"
 #include "sscan_mma.cuh"
 #include "sscan_tma.cuh"
@@ -38,57 +39,63 @@ struct HeadsArgs {
 };
 
 // Scalars of one chunk's steps, and their running sums (read two at a time, hence the alignment).
-struct alignas(16) ChunkScalars {
-    float ch[kQ], cl[kQ];     // log2(e) c_t as the sum of two floats: the difference of two of
+template <int Q>
+struct alignas(16) ChunkScalarsOf {
+    float ch[Q], cl[Q];     // log2(e) c_t as the sum of two floats: the difference of two of
                               // them keeps its absolute error near 2^-24 whatever c_t's size
-    float w[kQ];
-    float e[kQ];              // exp(c_t)
-    float d[kQ];              // exp(c_end - c_t)
-    float f[kQ];              // d_t w_t
+    float w[Q];
+    float e[Q];               // exp(c_t)
+    float d[Q];               // exp(c_end - c_t)
+    float f[Q];               // d_t w_t
     float total;              // c_end
 };
+using ChunkScalars = ChunkScalarsOf<kQ>;
 
 // What the gradients of the scalars need besides.
 struct ChunkSteps {
     float dl[kQ], raw[kQ];    // step sizes, and what softplus was taken of
 };
 
-// One warp fills s (and steps) for steps t0 .. t0 + kQ - 1 of (b, h); past L: q = w = 0.
-template <typename T>
-__device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& a, int64_t b, int h, int64_t t0,
+// One warp fills s (and steps) for steps t0 .. t0 + Q - 1 of (b, h); past L: q = w = 0.
+template <typename T, int Q>
+__device__ __forceinline__ void chunk_scalars(ChunkScalarsOf<Q>& s, const HeadsArgs& a, int64_t b, int h, int64_t t0,
                                               ChunkSteps* steps = nullptr) {
+    constexpr int PER = Q / 32;  // consecutive steps of a lane
     const int lane = threadIdx.x & 31;
     const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
     const T* dr = static_cast<const T*>(a.delta_raw);
-    double c[2];
-    float w[2];
+    double c[PER];
+    float w[PER];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t t = t0 + 2 * lane + i;
+    for (int i = 0; i < PER; ++i) {
+        const int64_t t = t0 + PER * lane + i;
         c[i] = 0.0;
         w[i] = 0.f;
-        if (steps) steps->dl[2 * lane + i] = steps->raw[2 * lane + i] = 0.f;
+        if (steps) steps->dl[PER * lane + i] = steps->raw[PER * lane + i] = 0.f;
         if (t < a.L) {
             const float r = IO<T>::load(dr, (b * a.L + t) * a.H + h) + bias;
             const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
             const float q = dl * A;
             w[i] = A != 0.f ? expm1f(q) / A : dl;
             c[i] = q < -1e4f ? -1e4 : (double)q;  // exp(-1e4) is 0 in fp32; keeps sums finite
-            if (steps) steps->dl[2 * lane + i] = dl, steps->raw[2 * lane + i] = r;
+            if (steps) steps->dl[PER * lane + i] = dl, steps->raw[PER * lane + i] = r;
         }
+        if (i) c[i] += c[i - 1];
     }
-    c[1] += c[0];
-    double run = c[1];
+    double run = c[PER - 1];
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const double v = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += v;
     }
-    const double before = run - c[1], end = __shfl_sync(0xffffffffu, run, 31);
+    // (not run - c[PER - 1]: a NaN in a lane's later step would reach its earlier ones)
+    double before = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) before = 0.0;
+    const double end = __shfl_sync(0xffffffffu, run, 31);
     constexpr double l2e = 1.4426950408889634074;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
+    for (int i = 0; i < PER; ++i) {
+        const int t = PER * lane + i;
         const double ct = (before + c[i]) * l2e;
         s.ch[t] = (float)ct;
         s.cl[t] = (float)(ct - (double)s.ch[t]);
@@ -101,7 +108,8 @@ __device__ __forceinline__ void chunk_scalars(ChunkScalars& s, const HeadsArgs& 
 }
 
 // exp(c_t - c_s)
-__device__ __forceinline__ float chunk_decay(const ChunkScalars& s, int t, int u) {
+template <int Q>
+__device__ __forceinline__ float chunk_decay(const ChunkScalarsOf<Q>& s, int t, int u) {
     return ex2((s.ch[t] - s.ch[u]) + (s.cl[t] - s.cl[u]));
 }
 
@@ -193,6 +201,12 @@ sscan_status check_heads(const sscan_heads_problem* p);
 HeadsArgs heads_args(const sscan_heads_problem* p, const void* u, const void* delta_raw, const float* delta_bias,
                      const float* A, const void* B, const void* C, const float* D_skip, const void* z,
                      const float* h0);
+// The forward on tcgen05 (sscan_heads_tc.cu): bf16, more than 32 states, rows on 16-byte boundaries.
+// Its chunks are 128 steps; a.chunks, seg_chunks and nseg count those.
+constexpr int kTcQ = 128;
+cudaError_t launch_heads_tc(const HeadsArgs& a, bool local, cudaStream_t st);
+
+
 // Local states of every segment: forward (u, B) or, with dout, reverse (dout SiLU(z), C).
 cudaError_t launch_heads_local(const HeadsArgs& a, const void* dout, bool bf16, cudaStream_t st);
 

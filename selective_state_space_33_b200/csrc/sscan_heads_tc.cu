@@ -1,0 +1,509 @@
+// sscan_heads_tc.cu -- the forward of the multi-head recurrence (sscan_heads.cuh) on the 5th-generation
+// tensor cores, for bf16 I/O and more than 32 states.
+//
+// With 128 states the chunk's products are 2 x 128 x (128 + 3 x 64 + 64 + 64) x 128 operations against 48 KB
+// of traffic; as mma.sync they kept eight warps loading fragments (1470 us at 65536 steps, 24 heads, 128
+// states, issue slots 45% busy, tensor pipe under 40%).  Here one thread issues them from
+// shared memory and tensor memory, and the warps only do what is elementwise.
+//
+// A block walks the chunks (128 steps) of one (batch, head, segment).  Tiles are rows of 64 bf16 in the
+// 128-byte swizzle, as TMA writes them: such a tile is a K-major operand when its rows are
+// the operand's rows and an MN-major one when its rows are k, so no tile is transposed:
+//   G  = C B^T         rows t, columns s   (C, B K-major)                 tensor memory, 128 columns
+//   Ya = C S^T         rows t, columns p   (C K-major, S [n][p] MN-major)                  64
+//   Yb = M U           rows t, columns p   (M bf16 in tensor memory, U [s][p] MN-major)    64
+//   St = B^T (f U)     rows n, columns p   (B [s][n], f U [s][p], both MN-major)           64
+// y = exp(c) Ya + Yb.  f U goes in as three bf16 parts (24 bits: the state is an fp32 result), S and M
+// as one, each a rounding of the size of the output's own.  The state itself stays in fp32
+// registers, row n and half of the channels per thread.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "sscan_heads.cuh"
+#include "sscan_vec.cuh"
+
+namespace sscan {
+
+__device__ unsigned int g_device_error_heads = 0;
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kWork = 256;               // 8 warps: 4 quarters of the rows by 2 halves of the columns
+constexpr int kThreads = kWork + 32;     // and the scalars' warp
+constexpr int kTile = kTcQ * 64;         // elements of a tile of 128 rows
+constexpr uint32_t kColG = 0, kColM = 128, kColYa = 192, kColYb = 256, kColSt = 320, kCols = 512;
+
+struct TcSmem {
+    alignas(1024) bf16 x[2][kTile];
+    alignas(1024) bf16 z[2][kTile];      // the gate, then the outputs
+    alignas(1024) bf16 B[2][kTile];      // states 0..63 and 64..127
+    alignas(1024) bf16 C[2][kTile];
+    alignas(1024) bf16 f[3][kTile];      // f U in three parts
+    alignas(1024) bf16 S[kTile];         // [n][p]
+    ChunkScalarsOf<kTcQ> s[2];
+    alignas(8) uint64_t full_x[2], full_bc, done_g, done_ya, done_st, done_yb;
+    uint32_t tmem;
+};
+
+// --- tcgen05 -------------------------------------------------------------------------------
+
+// Shared-memory operand: 128-byte swizzle; lead: bytes between blocks of 64 along the operand's rows
+// or columns (MN-major only); groups of eight tile rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// bf16 x bf16 -> fp32, 128 rows by n columns; ta / tb: the operand is MN-major.
+__host__ __device__ constexpr uint32_t instruction(int n, int ta, int tb) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n / 8) << 17) |
+           ((128u / 16) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 rows.
+__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int t, int b, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(t), "r"(b), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int x, int y, int t, int b, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(t), "r"(b), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWork) : "memory"); }
+__device__ __forceinline__ int work_or(int v) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(v), "n"(kWork) : "memory");
+    return r;
+}
+
+// Byte offset of 16-byte unit c of row r of a tile.
+__device__ __forceinline__ uint32_t unit(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+
+// The terms M_ts u_s, s <= t, of one channel whose u_s is not finite, from global memory.
+__device__ __noinline__ float not_finite_terms(const HeadsArgs& a, const ChunkScalarsOf<kTcQ>& s, int64_t b, int h, int grp,
+                                               int64_t t0, int t, int p) {
+    const bf16 *u = static_cast<const bf16*>(a.u), *B = static_cast<const bf16*>(a.B), *C = static_cast<const bf16*>(a.C);
+    float v = 0.f;
+    for (int q = 0; q <= t; ++q) {
+        const float x = __bfloat162float(u[((b * a.L + t0 + q) * a.H + h) * a.P + p]);
+        if (fabsf(x) <= 3.4e38f) continue;
+        float dot = 0.f;
+        for (int n = 0; n < a.N; ++n)
+            dot = fmaf(__bfloat162float(C[((b * a.L + t0 + t) * a.G + grp) * a.N + n]),
+                       __bfloat162float(B[((b * a.L + t0 + q) * a.G + grp) * a.N + n]), dot);
+        v += dot * (chunk_decay(s, t, q) * s.w[q]) * x;
+    }
+    return v;
+}
+
+// kOut: outputs, from the state entering the segment; else the segment's end state from zero.
+template <int NT, bool kOut>
+__global__ void __launch_bounds__(kThreads, 1)
+    heads_tc_kernel(const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_z,
+                    const __grid_constant__ CUtensorMap tm_B, const __grid_constant__ CUtensorMap tm_C,
+                    const __grid_constant__ CUtensorMap tm_out, HeadsArgs a) {
+    constexpr int HALVES = NT / 64;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<TcSmem*>(smem_raw);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int64_t seg = blockIdx.x / a.H;
+    const int b = blockIdx.y, h = (int)(blockIdx.x - seg * a.H), grp = h / (a.H / a.G);
+    const int64_t c0 = seg * a.seg_chunks, c1 = c0 + a.seg_chunks < a.chunks ? c0 + a.seg_chunks : a.chunks;
+    const int n = (int)(c1 - c0);
+    const int64_t bh = (int64_t)b * a.H + h;
+    const bool gate = kOut && a.z;
+
+    if (tid == 0) {
+        for (uint64_t* bar : {&sm.full_x[0], &sm.full_x[1], &sm.full_bc, &sm.done_g, &sm.done_ya, &sm.done_st, &sm.done_yb})
+            mbar_init(smem_u32(bar), 1);
+        fence_proxy_async();
+    }
+    if (w == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "n"(kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    if (w == 8) {
+        // the scalars of chunk i + 1 while the others work on chunk i
+        chunk_scalars<bf16, kTcQ>(sm.s[0], a, b, h, c0 * kTcQ);
+        for (int i = 0; i < n; ++i) {
+            __syncthreads();
+            if (i + 1 < n) chunk_scalars<bf16, kTcQ>(sm.s[(i + 1) & 1], a, b, h, (c0 + i + 1) * kTcQ);
+        }
+        __syncthreads();
+        return;
+    }
+
+    auto fetch_x = [&](int i) {
+        const uint32_t bar = smem_u32(&sm.full_x[i & 1]);
+        const int t0 = (int)((c0 + i) * kTcQ);
+        mbar_expect_tx(bar, (gate ? 2 : 1) * kTile * 2);
+        tma_load_4d(smem_u32(sm.x[i & 1]), &tm_u, 0, h, t0, b, bar);
+        if (gate) tma_load_4d(smem_u32(sm.z[i & 1]), &tm_z, 0, h, t0, b, bar);
+    };
+    auto fetch_bc = [&](int i) {
+        const uint32_t bar = smem_u32(&sm.full_bc);
+        const int t0 = (int)((c0 + i) * kTcQ);
+        mbar_expect_tx(bar, (kOut ? 2 : 1) * HALVES * kTile * 2);
+        for (int k = 0; k < HALVES; ++k) {
+            tma_load_4d(smem_u32(sm.B[k]), &tm_B, 64 * k, grp, t0, b, bar);
+            if (kOut) tma_load_4d(smem_u32(sm.C[k]), &tm_C, 64 * k, grp, t0, b, bar);
+        }
+    };
+    bool late = false;  // a wait gave up: none is tried again, so that the block ends soon
+    auto wait = [&](uint64_t* bar, int phase) {
+        if (late || mbar_wait(smem_u32(bar), phase)) return;
+        late = true;
+        atomicOr(&g_device_error_heads, 1u);
+    };
+
+    const int quarter = w & 3, half = w >> 2, r = 32 * quarter + lane;   // this thread's row and half of the columns
+    const uint32_t tm_row = tmem + ((uint32_t)(32 * quarter) << 16);
+    if (tid == 0) {
+        fetch_x(0);
+        if (n > 1) fetch_x(1);
+        fetch_bc(0);
+    }
+
+    // the state: row n = r, channels 32 half .. + 31
+    float S[32];
+    {
+        const float* first = !kOut ? nullptr : a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N : a.h0 ? a.h0 + bh * a.P * a.N : nullptr;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const int p = 32 * half + k;
+            S[k] = first && r < a.N && p < a.P ? first[(int64_t)p * a.N + r] : 0.f;
+        }
+    }
+    auto put_state = [&] {  // bf16 S for Ya: row r of [n][p]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint4 v;
+            uint32_t* o = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = Mma<bf16>::pack(S[8 * k + 2 * i], S[8 * k + 2 * i + 1]);
+            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.S) + unit(r, 4 * half + k)) = v;
+        }
+    };
+    if (kOut) {
+        put_state();
+        fence_proxy_async();
+    }
+    double total = 0.0;
+
+    for (int i = 0; i < n; ++i) {
+        const int buf = i & 1, ph = i & 1;
+        const int64_t t0 = (c0 + i) * kTcQ;
+        __syncthreads();                       // this chunk's scalars; S of the last one is in shared memory
+        const auto& sc = sm.s[buf];
+        wait(&sm.full_x[buf], (i >> 1) & 1);
+        wait(&sm.full_bc, ph);
+        if (kOut && tid == 0) {
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < NT / 16; ++k)
+                mma_ss(tmem + kColG, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16), operand(smem_u32(sm.B[k / 4]) + 32 * (k % 4), 16),
+                       instruction(128, 0, 0), k > 0);
+            commit(&sm.done_g);
+#pragma unroll
+            for (int k = 0; k < NT / 16; ++k)
+                mma_ss(tmem + kColYa, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16), operand(smem_u32(sm.S) + 2048 * k, 16),
+                       instruction(64, 0, 1), k > 0);
+            commit(&sm.done_ya);
+        }
+        if (tid == 0 && i > 0 && i + 1 < n) {          // the buffers of the chunk before are free once its outputs have left
+            if (kOut) tma_store_wait_read_0();
+            fetch_x(i + 1);
+        }
+        // f U in three parts; values of u that are not finite are noticed on the way
+        float probe = 0.f;
+        unsigned char* xb = reinterpret_cast<unsigned char*>(sm.x[buf]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = (tid >> 3) + 32 * k;
+            const uint32_t at = unit(row, tid & 7);
+            float v[8];
+            widen8(*reinterpret_cast<const uint4*>(xb + at), v);
+            const float f = sc.f[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (kOut) probe = fmaf(v[e], 0.f, probe);
+                v[e] *= f;
+            }
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                uint4 o;
+                uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ow[e] = Mma<bf16>::pack(v[2 * e], v[2 * e + 1]);
+                    v[2 * e] -= __uint_as_float(ow[e] << 16);
+                    v[2 * e + 1] -= __uint_as_float(ow[e] & 0xffff0000u);
+                }
+                *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.f[part]) + at) = o;
+            }
+        }
+        fence_proxy_async();
+        int bad = 0;
+        if (kOut) bad = work_or(probe != 0.f);
+        else work_sync();
+        if (tid == 0) {
+            fence_after();
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+                for (int k = 0; k < kTcQ / 16; ++k)
+                    mma_ss(tmem + kColSt, operand(smem_u32(sm.B[0]) + 2048 * k, HALVES == 2 ? kTile * 2 : 0),
+                           operand(smem_u32(sm.f[part]) + 2048 * k, 16), instruction(64, 1, 1), part < 2 || k > 0);
+            commit(&sm.done_st);
+        }
+        if (kOut && bad) {
+            // Such a value would meet the zeros of M above the diagonal: it is left out of the product
+            // and its terms are added to the steps that have them, below.
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t at = unit((tid >> 3) + 32 * k, tid & 7);
+                uint32_t* v = reinterpret_cast<uint32_t*>(xb + at);
+                for (int e = 0; e < 4; ++e) {
+                    if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
+                    if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu;
+                }
+            }
+            fence_proxy_async();
+        }
+        if (kOut) {
+            // M: row t = r, columns s = 64 half .. + 63
+            wait(&sm.done_g, ph);
+            fence_after();
+            const float ch = sc.ch[r], cl = sc.cl[r];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int s0 = 64 * half + 32 * g;
+                uint32_t m[16];
+                if (s0 > 32 * quarter + 31) {          // all above the diagonal
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) m[k] = 0u;
+                } else {
+                    float v[32];
+                    tmem_load(v, tm_row + kColG + s0);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 chs = *reinterpret_cast<const float4*>(sc.ch + s0 + k);
+                        const float4 cls = *reinterpret_cast<const float4*>(sc.cl + s0 + k);
+                        const float4 ws = *reinterpret_cast<const float4*>(sc.w + s0 + k);
+                        const float cs[4] = {chs.x, chs.y, chs.z, chs.w}, ls[4] = {cls.x, cls.y, cls.z, cls.w},
+                                    wv[4] = {ws.x, ws.y, ws.z, ws.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[k + e] = s0 + k + e <= r ? v[k + e] * (ex2((ch - cs[e]) + (cl - ls[e])) * wv[e]) : 0.f;
+                        m[k / 2] = Mma<bf16>::pack(v[k], v[k + 1]);
+                        m[k / 2 + 1] = Mma<bf16>::pack(v[k + 2], v[k + 3]);
+                    }
+                }
+                tmem_store16(tm_row + kColM + s0 / 2, m);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            fence_before();
+            work_sync();
+            if (tid == 0) {
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < kTcQ / 16; ++k)
+                    mma_ts(tmem + kColYb, tmem + kColM + 8 * k, operand(smem_u32(sm.x[buf]) + 2048 * k, 16), instruction(64, 0, 1), k > 0);
+                commit(&sm.done_yb);
+            }
+        }
+        // S' = exp(c_end) S + B^T (f U)
+        wait(&sm.done_st, ph);
+        if (kOut) wait(&sm.done_ya, ph);
+        fence_after();
+        if (tid == 0 && i + 1 < n) fetch_bc(i + 1);    // every product that reads B and C is done
+        {
+            const float dec = ex2(sc.total * kLog2e);
+            total += sc.total;
+            float v[32];
+            tmem_load(v, tm_row + kColSt + 32 * half);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) S[k] = fmaf(dec, S[k], v[k]);
+        }
+        if (kOut) {
+            put_state();
+            wait(&sm.done_yb, ph);
+            fence_after();
+            float ya[32], yb[32];
+            tmem_load(ya, tm_row + kColYa + 32 * half);
+            tmem_load(yb, tm_row + kColYb + 32 * half);
+            const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
+            unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z[buf]);
+            // written twice: the calls of the rare form would cost the usual one its registers
+            auto outputs = [&](auto rare) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t at = unit(r, 4 * half + k);
+                    float xv[8], zv[8], y[8];
+                    widen8(*reinterpret_cast<const uint4*>(xb + at), xv);
+                    if (gate) widen8(*reinterpret_cast<const uint4*>(zb + at), zv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        y[j] = fmaf(e, ya[8 * k + j], yb[8 * k + j]);
+                        if constexpr (decltype(rare)::value) {
+                            const int p = 32 * half + 8 * k + j;
+                            if (t0 + r < a.L && p < a.P) {
+                                y[j] += not_finite_terms(a, sc, b, h, grp, t0, r, p);
+                                xv[j] = __bfloat162float(static_cast<const bf16*>(a.u)[((b * a.L + t0 + r) * a.H + h) * a.P + p]);
+                            }
+                        }
+                        if (a.D) y[j] = fmaf(D, xv[j], y[j]);
+                        if (gate) y[j] *= silu(zv[j]);
+                    }
+                    uint4 o;
+                    uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ow[j] = Mma<bf16>::pack(y[2 * j], y[2 * j + 1]);
+                    *reinterpret_cast<uint4*>(zb + at) = o;
+                }
+            };
+            if (bad) outputs(std::true_type{});
+            else outputs(std::false_type{});
+            fence_proxy_async();
+        }
+        fence_before();
+        work_sync();                                   // tensor memory and this chunk's tiles are read
+        if (kOut && tid == 0) tma_store_4d(&tm_out, 0, h, (int)t0, b, smem_u32(sm.z[buf]));
+    }
+    if (kOut) {
+        if (a.h_last && seg == a.nseg - 1 && r < a.N) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (32 * half + k < a.P) a.h_last[bh * a.P * a.N + (int64_t)(32 * half + k) * a.N + r] = S[k];
+        }
+        if (tid == 0) tma_store_wait_all();
+    } else {
+        if (r < a.N) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (32 * half + k < a.P) a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(32 * half + k) * a.N + r] = S[k];
+        }
+        if (tid == 0) a.decays[bh * a.nseg + seg] = (float)total;
+    }
+    __syncthreads();
+    if (w == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols));
+}
+
+// A map over (batch, L, heads or groups, width) with boxes of 128 steps by 64 of the width, zeros outside.
+bool tc_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t L, int64_t batch) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)L, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)(width * rows) * 2, (cuuint64_t)(width * rows * L) * 2};
+    const cuuint32_t box[4] = {64, 1, kTcQ, 1}, each[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, each,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool kOut>
+cudaError_t launch(const HeadsArgs& a, cudaStream_t st) {
+    CUtensorMap m[5];
+    if (!tc_map(&m[0], a.u, a.P, a.H, a.L, a.batch) || !tc_map(&m[1], a.z ? a.z : a.u, a.P, a.H, a.L, a.batch) ||
+        !tc_map(&m[2], a.B, a.N, a.G, a.L, a.batch) || !tc_map(&m[3], a.C, a.N, a.G, a.L, a.batch) ||
+        !tc_map(&m[4], a.out ? a.out : a.u, a.P, a.H, a.L, a.batch))
+        return cudaErrorInvalidValue;
+    auto* k = heads_tc_kernel<NT, kOut>;
+    constexpr size_t smem = sizeof(TcSmem);
+    static_assert(smem <= 227 * 1024, "the tiles of one chunk must fit a block's shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k<<<dim3((unsigned)(a.H * a.nseg), (unsigned)a.batch), kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], a);
+    api_count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_heads_tc(const HeadsArgs& a, bool local, cudaStream_t st) {
+    if (a.N <= 64) return local ? launch<64, false>(a, st) : launch<64, true>(a, st);
+    return local ? launch<128, false>(a, st) : launch<128, true>(a, st);
+}
+
+cudaError_t read_device_error_heads(unsigned int* value, int clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error_heads, sizeof(unsigned int));
+    if (e == cudaSuccess && clear && *value) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error_heads, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+}  // namespace sscan

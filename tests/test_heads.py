@@ -37,7 +37,10 @@ NAMES = {"du": "u", "ddelta_raw": "delta_raw", "dA": "A", "dB": "B", "dC": "C", 
          "dD": "D_skip", "dz": "z", "dh0": "h0"}
 # batch, L, heads, P, N, groups: around the 64-step chunk; P, N off every multiple
 SHAPES = [(1, 1, 1, 1, 1, 1), (2, 7, 3, 64, 16, 1), (1, 63, 2, 16, 40, 2), (2, 64, 4, 33, 5, 2), (1, 65, 1, 64, 128, 1),
-          (1, 200, 6, 40, 24, 3), (2, 130, 2, 64, 64, 1), (1, 321, 2, 8, 100, 1), (1, 700, 2, 20, 16, 1)]
+          (1, 200, 6, 40, 24, 3), (2, 130, 2, 64, 64, 1), (1, 321, 2, 8, 100, 1), (1, 700, 2, 20, 16, 1),
+          # more than 32 states on 16-byte rows, around the 128-step chunk of the tensor-core forward
+          (1, 128, 2, 64, 128, 1), (2, 129, 1, 48, 72, 1), (1, 255, 4, 64, 64, 2), (1, 700, 2, 64, 128, 1),
+          (1, 1100, 3, 16, 48, 3)]
 
 
 def case(shape, seed, io, device, **kw):
@@ -151,15 +154,17 @@ def test_steps_and_segments_equal_one_forward(cuda_device, io, P, N):
 @pytest.mark.gpu
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
-def test_a_value_that_is_not_finite_stays_in_its_own_future(cuda_device, io, value):
-    x = case((2, 150, 2, 16, 16, 1), 9, io, cuda_device)
+@pytest.mark.parametrize("N", [16, 64])
+def test_a_value_that_is_not_finite_stays_in_its_own_future(cuda_device, io, value, N):
+    x = case((2, 150, 2, 16, N, 1), 9, io, cuda_device)
     clean = sb.sscan_heads_fwd(**x)
     for name, at in (("u", (1, 70, 1, 3)), ("B", (1, 70, 0, 2)), ("C", (1, 70, 0, 2)), ("z", (1, 70, 1, 3)),
-                     ("delta_raw", (1, 70, 1))):
+                     ("delta_raw", (1, 70, 1)), ("delta_raw", (1, 71, 1))):
         y = dict(x)
         y[name] = x[name].clone()
         y[name][at] = value
         out = sb.sscan_heads_fwd(**y)
+        assert sb.device_status() == 0
         assert torch.equal(out[0], clean[0]), name
         assert torch.equal(out[1, :70], clean[1, :70]), name
         if name in ("u", "z", "delta_raw"):              # the other head
