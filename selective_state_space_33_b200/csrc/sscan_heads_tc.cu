@@ -34,19 +34,20 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kWork = 256;               // 8 warps: 4 quarters of the rows by 2 halves of the columns
-constexpr int kThreads = kWork + 32;     // and the scalars' warp
+constexpr int kIssue = kWork + 32;       // and the warp that issues products and copies
+constexpr int kThreads = kIssue + 64;    // and one each for the scalars of even and odd chunks
 constexpr int kTile = kTcQ * 64;         // elements of a tile of 128 rows
 constexpr uint32_t kColG = 0, kColM = 128, kColYa = 192, kColYb = 256, kColSt = 320, kCols = 512;
 
 struct TcSmem {
-    alignas(1024) bf16 x[2][kTile];
-    alignas(1024) bf16 z[2][kTile];      // the gate, then the outputs
-    alignas(1024) bf16 B[2][kTile];      // states 0..63 and 64..127
+    alignas(1024) bf16 x[2][kTile];      // by chunk, as B
+    alignas(1024) bf16 B[2][2][kTile];   // states 0..63 and 64..127
     alignas(1024) bf16 C[2][kTile];
+    alignas(1024) bf16 z[kTile];         // the gate, then the outputs
     alignas(1024) bf16 f[3][kTile];      // f U in three parts
     alignas(1024) bf16 S[kTile];         // [n][p]
-    ChunkScalarsOf<kTcQ> s[2];
-    alignas(8) uint64_t full_x[2], full_bc, done_g, done_ya, done_st, done_yb;
+    ChunkScalarsOf<kTcQ> s[4];           // by chunk
+    alignas(8) uint64_t full_x[2], full_b[2], full_c, full_z, scalars_ready[4], scalars_free[4], done_g, done_ya, done_st, done_yb;
     uint32_t tmem;
 };
 
@@ -123,12 +124,17 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, int x, int 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWork) : "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The working warps and the issuing one keep step: three barriers a chunk.
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kIssue) : "memory"); }
 __device__ __forceinline__ int work_or(int v) {
     int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"(v), "n"(kWork) : "memory");
+        : "=r"(r) : "r"(v), "n"(kIssue) : "memory");
     return r;
 }
 
@@ -176,8 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool gate = kOut && a.z;
 
     if (tid == 0) {
-        for (uint64_t* bar : {&sm.full_x[0], &sm.full_x[1], &sm.full_bc, &sm.done_g, &sm.done_ya, &sm.done_st, &sm.done_yb})
-            mbar_init(smem_u32(bar), 1);
+        for (uint64_t* bar = &sm.full_x[0]; bar <= &sm.done_yb; ++bar) mbar_init(smem_u32(bar), 1);
         fence_proxy_async();
     }
     if (w == 0) {
@@ -189,48 +194,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = sm.tmem;
 
-    if (w == 8) {
-        // the scalars of chunk i + 1 while the others work on chunk i
-        chunk_scalars<bf16, kTcQ>(sm.s[0], a, b, h, c0 * kTcQ);
-        for (int i = 0; i < n; ++i) {
-            __syncthreads();
-            if (i + 1 < n) chunk_scalars<bf16, kTcQ>(sm.s[(i + 1) & 1], a, b, h, (c0 + i + 1) * kTcQ);
-        }
-        __syncthreads();
-        return;
-    }
-
-    auto fetch_x = [&](int i) {
-        const uint32_t bar = smem_u32(&sm.full_x[i & 1]);
-        const int t0 = (int)((c0 + i) * kTcQ);
-        mbar_expect_tx(bar, (gate ? 2 : 1) * kTile * 2);
-        tma_load_4d(smem_u32(sm.x[i & 1]), &tm_u, 0, h, t0, b, bar);
-        if (gate) tma_load_4d(smem_u32(sm.z[i & 1]), &tm_z, 0, h, t0, b, bar);
-    };
-    auto fetch_bc = [&](int i) {
-        const uint32_t bar = smem_u32(&sm.full_bc);
-        const int t0 = (int)((c0 + i) * kTcQ);
-        mbar_expect_tx(bar, (kOut ? 2 : 1) * HALVES * kTile * 2);
-        for (int k = 0; k < HALVES; ++k) {
-            tma_load_4d(smem_u32(sm.B[k]), &tm_B, 64 * k, grp, t0, b, bar);
-            if (kOut) tma_load_4d(smem_u32(sm.C[k]), &tm_C, 64 * k, grp, t0, b, bar);
-        }
-    };
     bool late = false;  // a wait gave up: none is tried again, so that the block ends soon
     auto wait = [&](uint64_t* bar, int phase) {
-        if (late || mbar_wait(smem_u32(bar), phase)) return;
+        if (late || mbar_wait(smem_u32(bar), phase & 1)) return;
         late = true;
         atomicOr(&g_device_error_heads, 1u);
     };
 
-    const int quarter = w & 3, half = w >> 2, r = 32 * quarter + lane;   // this thread's row and half of the columns
-    const uint32_t tm_row = tmem + ((uint32_t)(32 * quarter) << 16);
-    if (tid == 0) {
-        fetch_x(0);
-        if (n > 1) fetch_x(1);
-        fetch_bc(0);
+    if (w > 8) {
+        // the scalars, up to four chunks ahead: a long chain of dependent operations (fp64 sums)
+        for (int i = w - 9; i < n; i += 2) {
+            if (i > 3) wait(&sm.scalars_free[i & 3], (i - 4) >> 2);
+            chunk_scalars<bf16, kTcQ>(sm.s[i & 3], a, b, h, (c0 + i) * kTcQ);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.scalars_ready[i & 3]);
+        }
+        __syncthreads();
+        return;
+    }
+    if (w == 8) {
+        // one lane issues; the warp keeps the barriers
+        const bool one = lane == 0;
+        auto at = [&](int i) { return (int)((c0 + i) * kTcQ); };
+        auto fetch = [&](bf16 (*dst)[kTile], int tiles, const CUtensorMap* map, int row, int i, uint64_t* bar) {
+            mbar_expect_tx(smem_u32(bar), tiles * kTile * 2);
+            for (int k = 0; k < tiles; ++k) tma_load_4d(smem_u32(dst[k]), map, 64 * k, row, at(i), b, smem_u32(bar));
+        };
+        if (one) {
+            fetch(&sm.x[0], 1, &tm_u, h, 0, &sm.full_x[0]);
+            fetch(sm.B[0], HALVES, &tm_B, grp, 0, &sm.full_b[0]);
+            if (kOut) fetch(sm.C, HALVES, &tm_C, grp, 0, &sm.full_c);
+        }
+        for (int i = 0; i < n; ++i) {
+            const int buf = i & 1;
+            work_sync();                       // the last chunk is done with
+            if (one) {
+                if (i > 0) mbar_arrive(&sm.scalars_free[(i - 1) & 3]);
+                if (kOut) {
+                    wait(&sm.full_b[buf], i >> 1);
+                    wait(&sm.full_c, i);
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < NT / 16; ++k)
+                        mma_ss(tmem + kColG, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16),
+                               operand(smem_u32(sm.B[buf][k / 4]) + 32 * (k % 4), 16), instruction(128, 0, 0), k > 0);
+                    commit(&sm.done_g);
+#pragma unroll
+                    for (int k = 0; k < NT / 16; ++k)
+                        mma_ss(tmem + kColYa, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16), operand(smem_u32(sm.S) + 2048 * k, 16),
+                               instruction(64, 0, 1), k > 0);
+                    commit(&sm.done_ya);
+                    if (i > 0) tma_store_4d(&tm_out, 0, h, at(i - 1), b, smem_u32(sm.z));
+                }
+                if (i + 1 < n) {
+                    fetch(&sm.x[buf ^ 1], 1, &tm_u, h, i + 1, &sm.full_x[buf ^ 1]);
+                    fetch(sm.B[buf ^ 1], HALVES, &tm_B, grp, i + 1, &sm.full_b[buf ^ 1]);
+                }
+                if (kOut) {
+                    tma_store_wait_read_0();
+                    if (gate) fetch(&sm.z, 1, &tm_z, h, i, &sm.full_z);
+                    else mbar_arrive(&sm.full_z);
+                }
+            }
+            __syncwarp();
+            if (kOut) work_or(0);
+            else work_sync();
+            if (one) {
+                if (!kOut) wait(&sm.full_b[buf], i >> 1);
+                fence_after();
+                for (int part = 2; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < kTcQ / 16; ++k)
+                        mma_ss(tmem + kColSt, operand(smem_u32(sm.B[buf][0]) + 2048 * k, HALVES == 2 ? kTile * 2 : 0),
+                               operand(smem_u32(sm.f[part]) + 2048 * k, 16), instruction(64, 1, 1), part < 2 || k > 0);
+                commit(&sm.done_st);
+                if (kOut && i + 1 < n) {
+                    wait(&sm.done_ya, i);
+                    fetch(sm.C, HALVES, &tm_C, grp, i + 1, &sm.full_c);
+                }
+            }
+            __syncwarp();
+            if (kOut) {
+                work_sync();
+                if (one) {
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < kTcQ / 16; ++k)
+                        mma_ts(tmem + kColYb, tmem + kColM + 8 * k, operand(smem_u32(sm.x[buf]) + 2048 * k, 16), instruction(64, 0, 1), k > 0);
+                    commit(&sm.done_yb);
+                }
+                __syncwarp();
+            }
+        }
+        if (kOut) {
+            work_sync();
+            if (one) {
+                tma_store_4d(&tm_out, 0, h, at(n - 1), b, smem_u32(sm.z));
+                tma_store_wait_all();
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+        return;
     }
 
+    const int quarter = w & 3, half = w >> 2, r = 32 * quarter + lane;   // this thread's row and half of the columns
+    const uint32_t tm_row = tmem + ((uint32_t)(32 * quarter) << 16);
     // the state: row n = r, channels 32 half .. + 31
     float S[32];
     {
@@ -258,29 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     double total = 0.0;
 
     for (int i = 0; i < n; ++i) {
-        const int buf = i & 1, ph = i & 1;
+        const int buf = i & 1;
         const int64_t t0 = (c0 + i) * kTcQ;
-        __syncthreads();                       // this chunk's scalars; S of the last one is in shared memory
-        const auto& sc = sm.s[buf];
-        wait(&sm.full_x[buf], (i >> 1) & 1);
-        wait(&sm.full_bc, ph);
-        if (kOut && tid == 0) {
-            fence_after();
-#pragma unroll
-            for (int k = 0; k < NT / 16; ++k)
-                mma_ss(tmem + kColG, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16), operand(smem_u32(sm.B[k / 4]) + 32 * (k % 4), 16),
-                       instruction(128, 0, 0), k > 0);
-            commit(&sm.done_g);
-#pragma unroll
-            for (int k = 0; k < NT / 16; ++k)
-                mma_ss(tmem + kColYa, operand(smem_u32(sm.C[k / 4]) + 32 * (k % 4), 16), operand(smem_u32(sm.S) + 2048 * k, 16),
-                       instruction(64, 0, 1), k > 0);
-            commit(&sm.done_ya);
-        }
-        if (tid == 0 && i > 0 && i + 1 < n) {          // the buffers of the chunk before are free once its outputs have left
-            if (kOut) tma_store_wait_read_0();
-            fetch_x(i + 1);
-        }
+        fence_before();
+        work_sync();                           // tensor memory, tiles and outputs of the last chunk are done with; S is there
+        const auto& sc = sm.s[i & 3];
+        wait(&sm.scalars_ready[i & 3], i >> 2);
+        wait(&sm.full_x[buf], i >> 1);
         // f U in three parts; values of u that are not finite are noticed on the way
         float probe = 0.f;
         unsigned char* xb = reinterpret_cast<unsigned char*>(sm.x[buf]);
@@ -313,15 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         int bad = 0;
         if (kOut) bad = work_or(probe != 0.f);
         else work_sync();
-        if (tid == 0) {
-            fence_after();
-            for (int part = 2; part >= 0; --part)
-#pragma unroll
-                for (int k = 0; k < kTcQ / 16; ++k)
-                    mma_ss(tmem + kColSt, operand(smem_u32(sm.B[0]) + 2048 * k, HALVES == 2 ? kTile * 2 : 0),
-                           operand(smem_u32(sm.f[part]) + 2048 * k, 16), instruction(64, 1, 1), part < 2 || k > 0);
-            commit(&sm.done_st);
-        }
         if (kOut && bad) {
             // Such a value would meet the zeros of M above the diagonal: it is left out of the product
             // and its terms are added to the steps that have them, below.
@@ -337,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kOut) {
             // M: row t = r, columns s = 64 half .. + 63
-            wait(&sm.done_g, ph);
+            wait(&sm.done_g, i);
             fence_after();
             const float ch = sc.ch[r], cl = sc.cl[r];
 #pragma unroll
@@ -369,19 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             work_sync();
-            if (tid == 0) {
-                fence_after();
-#pragma unroll
-                for (int k = 0; k < kTcQ / 16; ++k)
-                    mma_ts(tmem + kColYb, tmem + kColM + 8 * k, operand(smem_u32(sm.x[buf]) + 2048 * k, 16), instruction(64, 0, 1), k > 0);
-                commit(&sm.done_yb);
-            }
         }
         // S' = exp(c_end) S + B^T (f U)
-        wait(&sm.done_st, ph);
-        if (kOut) wait(&sm.done_ya, ph);
+        wait(&sm.done_st, i);
+        if (kOut) wait(&sm.done_ya, i);
         fence_after();
-        if (tid == 0 && i + 1 < n) fetch_bc(i + 1);    // every product that reads B and C is done
         {
             const float dec = ex2(sc.total * kLog2e);
             total += sc.total;
@@ -392,13 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kOut) {
             put_state();
-            wait(&sm.done_yb, ph);
+            wait(&sm.done_yb, i);
+            wait(&sm.full_z, i);
             fence_after();
             float ya[32], yb[32];
             tmem_load(ya, tm_row + kColYa + 32 * half);
             tmem_load(yb, tm_row + kColYb + 32 * half);
             const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
-            unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z[buf]);
+            unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z);
             // written twice: the calls of the rare form would cost the usual one its registers
             auto outputs = [&](auto rare) {
 #pragma unroll
@@ -431,9 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             else outputs(std::false_type{});
             fence_proxy_async();
         }
-        fence_before();
-        work_sync();                                   // tensor memory and this chunk's tiles are read
-        if (kOut && tid == 0) tma_store_4d(&tm_out, 0, h, (int)t0, b, smem_u32(sm.z[buf]));
     }
     if (kOut) {
         if (a.h_last && seg == a.nseg - 1 && r < a.N) {
@@ -441,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 32; ++k)
                 if (32 * half + k < a.P) a.h_last[bh * a.P * a.N + (int64_t)(32 * half + k) * a.N + r] = S[k];
         }
-        if (tid == 0) tma_store_wait_all();
+        work_sync();                           // the last chunk's outputs may leave
     } else {
         if (r < a.N) {
 #pragma unroll
