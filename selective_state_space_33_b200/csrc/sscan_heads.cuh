@@ -173,18 +173,21 @@ __device__ __forceinline__ void load_rows_async(T* dst, int pitch, const T* src,
     }
 }
 
-// Neighbouring values x, y as hi + lo in the tile type: bf16 keeps 16 bits in the two (a relative
-// 2^-17), which is what an fp32 sum needs from a factor that is not itself a bf16 input; an fp32
-// tile needs no second part.
+// Neighbouring values x, y in the tile type: fp32 as they are; bf16 as two parts, which keep 16
+// bits (a relative 2^-17), and what they leave, rounded to a third (24 bits).
 template <typename T>
-__device__ __forceinline__ void split_store2(T* hi, T* lo, int at, float x, float y) {
+__device__ __forceinline__ uint32_t split_store2(T* hi, T* lo, int at, float x, float y) {
     if constexpr (Mma<T>::kExact32) {
         *reinterpret_cast<float2*>(hi + at) = make_float2(x, y);
+        return 0u;
     } else {
         const uint32_t h = Mma<T>::pack(x, y);
         *reinterpret_cast<uint32_t*>(hi + at) = h;
-        *reinterpret_cast<uint32_t*>(lo + at) =
-            Mma<T>::pack(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
+        x -= __uint_as_float(h << 16);
+        y -= __uint_as_float(h & 0xffff0000u);
+        const uint32_t l = Mma<T>::pack(x, y);
+        *reinterpret_cast<uint32_t*>(lo + at) = l;
+        return Mma<T>::pack(x - __uint_as_float(l << 16), y - __uint_as_float(l & 0xffff0000u));
     }
 }
 

@@ -12,9 +12,11 @@
 //   dq_t = sum_{t' >= t} dc_t',   dw_t = sum_t' G H E (column t) + d_t u_t . R B_t
 //   ddelta = dq A + dw exp(q),    dA = sum dq delta + dw dw/dA.
 // A block takes one chunk of one batch row and a share of the heads of a group; dB and dC are
-// accumulated over its heads in registers.  dA, ddelta_bias and dh0 are fp32 sums over the
-// whole sequence, so everything that feeds them (H, S C, R B) takes its inexact factor as two
-// bf16 parts; M1, M2 and the factors of the products that end in bf16 are rounded once.
+// accumulated over its heads in registers.  dA and ddelta_bias are fp32 sums over the whole
+// sequence of differences that nearly cancel (with two bf16 parts, 16 bits, a bias gradient came out
+// 8e-5 off where the same sums in fp32 lose 1e-6), so everything that feeds them (H, S C, R B)
+// takes its inexact factor as three bf16 parts, 24 bits; M1, M2 and the factors of the
+// products that end in bf16 are rounded once.
 #include <cuda_runtime.h>
 
 #include "sscan_heads.cuh"
@@ -52,8 +54,10 @@ struct BwdSmem {
     alignas(16) T sl[two ? kHeadDim * Pt::N : 1];
     alignas(16) T rh[kHeadDim * Pt::N];          // R, [p][n]
     alignas(16) T rl[two ? kHeadDim * Pt::N : 1];
-    alignas(16) T m1[kQ * Pt::Q];                // [t][s]
-    alignas(16) T m2[kQ * Pt::Q];
+    // M1 and M2, [t][s]; before them, in bf16, the third parts of R and S, and then of dy
+    static constexpr int M = two && Pt::N > Pt::Q ? kHeadDim * Pt::N : kQ * Pt::Q;
+    alignas(16) T m1[M];
+    alignas(16) T m2[M];
     ChunkScalars s;
     ChunkSteps steps;
     float row[2][kQ], col[4][kQ], qs[2][kQ], rs[2][kQ];
@@ -88,9 +92,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Loads a P x N fp32 state into two tiles of T ([p][n], zero-padded).
+// Loads a P x N fp32 state into its parts, tiles of T ([p][n], zero-padded).
 template <typename T, int NT, typename Each>
-__device__ __forceinline__ void load_state(T* hi, T* lo, const float* src, int P, int N, int tid, Each each) {
+__device__ __forceinline__ void load_state(T* hi, T* lo, T* third, const float* src, int P, int N, int tid, Each each) {
     constexpr int pitch = HeadsPitch<T, NT>::N;
     for (int i = tid; i < kHeadDim * NT / 4; i += kThreads) {
         const int p = i / (NT / 4), n = (i - p * (NT / 4)) * 4;
@@ -107,7 +111,10 @@ __device__ __forceinline__ void load_state(T* hi, T* lo, const float* src, int P
             }
         }
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) split_store2<T>(hi, lo, p * pitch + n + k, v[k], v[k + 1]);
+        for (int k = 0; k < 4; k += 2) {
+            const uint32_t t = split_store2<T>(hi, lo, p * pitch + n + k, v[k], v[k + 1]);
+            if constexpr (!Mma<T>::kExact32) *reinterpret_cast<uint32_t*>(third + p * pitch + n + k) = t;
+        }
         each(i, v);
     }
 }
@@ -149,10 +156,12 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
         if (w == 0) chunk_scalars<T>(sm.s, a, b, h, t0, &sm.steps);
         // u, dy and their product's sum
         float dsum = 0.f, ssum = 0.f;
+        constexpr int VE = 16 / sizeof(T), PER = kHeadDim / VE, LOADS = kQ * PER / kThreads;
+        uint32_t dy3[M::kExact32 ? 1 : LOADS][VE / 2];   // third parts of dy, for later
         {
-            constexpr int VE = 16 / sizeof(T), PER = kHeadDim / VE;
-            for (int i = tid; i < kQ * PER; i += kThreads) {
-                const int t = i / PER, p = (i - t * PER) * VE;
+#pragma unroll
+            for (int n = 0; n < LOADS; ++n) {
+                const int i = tid + n * kThreads, t = i / PER, p = (i - t * PER) * VE;
                 const int64_t at = ((tok + t) * a.H + h) * a.P + p;
                 float xv[VE], dv[VE], zv[VE];
                 if (t < rows && p < a.P && a.vec) {
@@ -172,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                 for (int j = 0; j < VE; j += 2) {
                     if (z) dv[j] *= silu(zv[j]), dv[j + 1] *= silu(zv[j + 1]);
                     dsum = fmaf(dv[j], xv[j], fmaf(dv[j + 1], xv[j + 1], dsum));
-                    split_store2<T>(sm.dyh, sm.dyl, t * Pt::P + p + j, dv[j], dv[j + 1]);
+                    const uint32_t third = split_store2<T>(sm.dyh, sm.dyl, t * Pt::P + p + j, dv[j], dv[j + 1]);
+                    if constexpr (!M::kExact32) dy3[n][j / 2] = third;
                 }
                 store_vec<VE>(sm.x + t * Pt::P + p, xv);
             }
@@ -182,13 +192,13 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             const int64_t at = (bh * a.chunks + c) * a.P * a.N;
             constexpr int PER = kHeadDim * NT / 4 / kThreads;
             float sv[PER][4];
-            load_state<T, NT>(sm.sh, sm.sl, a.states + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
+            load_state<T, NT>(sm.sh, sm.sl, sm.m2, a.states + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     if (i == tid + j * kThreads)
                         for (int e = 0; e < 4; ++e) sv[j][e] = v[e];
             });
-            load_state<T, NT>(sm.rh, sm.rl, k.R + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
+            load_state<T, NT>(sm.rh, sm.rl, sm.m1, k.R + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     if (i == tid + j * kThreads)
@@ -245,14 +255,85 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             }
         };
 
+        // R B (rows s, columns p) and S C (rows t, columns p): both end in fp32 sums over the sequence
+        // that nearly cancel, so R, S and dy enter with 24 bits
+        float x[4][4], y[4][4];
+        {
+            zero_acc(x);
+            warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.rh, Pt::N, 32 * wc, 0, NT);
+            if constexpr (!M::kExact32) {
+                warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.rl, Pt::N, 32 * wc, 0, NT);
+                warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.m1, Pt::N, 32 * wc, 0, NT);
+            }
+            float va = 0.f, vb = 0.f;
+            const float fa = sm.s.f[ra], fb = sm.s.f[rb];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float u0[2], u1[2];
+                load_shared<2>(sm.x + ra * Pt::P + cb + 8 * j, u0);
+                load_shared<2>(sm.x + rb * Pt::P + cb + 8 * j, u1);
+                va = fmaf(x[j][0], u0[0], fmaf(x[j][1], u0[1], va));
+                vb = fmaf(x[j][2], u1[0], fmaf(x[j][3], u1[1], vb));
+                x[j][0] *= fa, x[j][1] *= fa;
+                x[j][2] *= fb, x[j][3] *= fb;
+            }
+            va = quad_sum(va);
+            vb = quad_sum(vb);
+            if (q == 0) sm.rs[wc][ra] = va, sm.rs[wc][rb] = vb;
+            zero_acc(y);
+            warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
+            if constexpr (!M::kExact32) {
+                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sl, Pt::N, 32 * wc, 0, NT);
+                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.m2, Pt::N, 32 * wc, 0, NT);
+            }
+            const float ea = sm.s.e[ra], eb = sm.s.e[rb];
+            va = vb = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const int at = (i ? rb : ra) * Pt::P + cb + 8 * j;
+                    float dy[2];
+                    load_shared<2>(sm.dyh + at, dy);
+                    if constexpr (!M::kExact32) {
+                        float lo[2];
+                        load_shared<2>(sm.dyl + at, lo);
+                        dy[0] += lo[0], dy[1] += lo[1];
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        y[j][i + n] *= i ? eb : ea;
+                        (i ? vb : va) += y[j][i + n] * dy[n];
+                        x[j][i + n] = fmaf(D, dy[n], x[j][i + n]);
+                    }
+                }
+            va = quad_sum(va);
+            vb = quad_sum(vb);
+            if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
+        }
+        if (!M::kExact32 && z) {
+            // the third part of dy takes the place of R's
+            __syncthreads();
+            if constexpr (!M::kExact32) {
+#pragma unroll
+                for (int n = 0; n < LOADS; ++n) {
+                    const int i = tid + n * kThreads, t = i / PER, p = (i - t * PER) * VE;
+                    *reinterpret_cast<uint4*>(sm.m1 + t * Pt::P + p) = make_uint4(dy3[n][0], dy3[n][1], dy3[n][2], dy3[n][3]);
+                }
+            }
+            __syncthreads();
+        }
         // H, then M1, M2 and the sums of G H E over rows and columns
         float Hm[4][4];
         zero_acc(Hm);
         if (lower) {
             warp_gemm<T, false, false, 4>(Hm, sm.dyh, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
-            if (!M::kExact32 && z)
+            if (!M::kExact32 && z) {
                 warp_gemm<T, false, false, 4>(Hm, sm.dyl, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
+                warp_gemm<T, false, false, 4>(Hm, sm.m1, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
+            }
         }
+        if constexpr (!M::kExact32) __syncthreads();  // the third parts are read
         float rowa = 0.f, rowb = 0.f;
         const float cha = sm.s.ch[ra], cla = sm.s.cl[ra], chb = sm.s.ch[rb], clb = sm.s.cl[rb];
 #pragma unroll
@@ -294,59 +375,9 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
         if (q == 0) sm.row[wc][ra] = rowa, sm.row[wc][rb] = rowb;
         __syncthreads();
 
-        // du: rows s, columns p; then S C and, with a gate, dz
+        // du, and with a gate dz
         {
-            float x[4][4];
-            zero_acc(x);
-            warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.rh, Pt::N, 32 * wc, 0, NT);
-            if constexpr (!M::kExact32)
-                warp_gemm<T, false, false, 4>(x, sm.B, Pt::N, 16 * wr, sm.rl, Pt::N, 32 * wc, 0, NT);
-            float va = 0.f, vb = 0.f;
-            const float fa = sm.s.f[ra], fb = sm.s.f[rb];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float u0[2], u1[2];
-                load_shared<2>(sm.x + ra * Pt::P + cb + 8 * j, u0);
-                load_shared<2>(sm.x + rb * Pt::P + cb + 8 * j, u1);
-                va = fmaf(x[j][0], u0[0], fmaf(x[j][1], u0[1], va));
-                vb = fmaf(x[j][2], u1[0], fmaf(x[j][3], u1[1], vb));
-                x[j][0] *= fa, x[j][1] *= fa;
-                x[j][2] *= fb, x[j][3] *= fb;
-            }
-            va = quad_sum(va);
-            vb = quad_sum(vb);
-            if (q == 0) sm.rs[wc][ra] = va, sm.rs[wc][rb] = vb;
             warp_gemm<T, true, true, 4>(x, sm.m1, Pt::Q, 16 * wr, sm.dyh, Pt::P, 32 * wc, 16 * wr, kQ);
-            // S C: rows t, columns p
-            float y[4][4];
-            zero_acc(y);
-            warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
-            if constexpr (!M::kExact32)
-                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sl, Pt::N, 32 * wc, 0, NT);
-            const float ea = sm.s.e[ra], eb = sm.s.e[rb];
-            va = vb = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const int at = (i ? rb : ra) * Pt::P + cb + 8 * j;
-                    float dy[2];
-                    load_shared<2>(sm.dyh + at, dy);
-                    if constexpr (!M::kExact32) {
-                        float lo[2];
-                        load_shared<2>(sm.dyl + at, lo);
-                        dy[0] += lo[0], dy[1] += lo[1];
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        y[j][i + n] *= i ? eb : ea;
-                        (i ? vb : va) += y[j][i + n] * dy[n];
-                        x[j][i + n] = fmaf(D, dy[n], x[j][i + n]);
-                    }
-                }
-            va = quad_sum(va);
-            vb = quad_sum(vb);
-            if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
             store_part(static_cast<T*>(k.du), x);
             if (z) {
                 // dout and z again, in this warp's layout, ahead of the product that hides their latency
@@ -394,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             float v[HTL][4];
             zero_acc(v);
             if (wc == 0) warp_gemm<T, false, true, HTL>(v, sm.dyh, Pt::P, 16 * wr, sm.sh, Pt::N, 8 * n0, 0, kHeadDim);
-            else warp_gemm<T, false, true, HTL>(v, sm.x, Pt::P, 16 * wr, sm.rh, Pt::N, 8 * n0, 0, kHeadDim);
+            // with a gate dy is not exact either: the second part of S keeps dC to two roundings, as dB
+            if (!M::kExact32 && z && wc == 0)
+                warp_gemm<T, false, true, HTL>(v, sm.dyh, Pt::P, 16 * wr, sm.sl, Pt::N, 8 * n0, 0, kHeadDim);
+            if (wc != 0) warp_gemm<T, false, true, HTL>(v, sm.x, Pt::P, 16 * wr, sm.rh, Pt::N, 8 * n0, 0, kHeadDim);
             const float fa = wc == 0 ? sm.s.e[ra] : sm.s.f[ra], fb = wc == 0 ? sm.s.e[rb] : sm.s.f[rb];
 #pragma unroll
             for (int j = 0; j < HTL; ++j) {

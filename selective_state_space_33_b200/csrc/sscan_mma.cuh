@@ -15,6 +15,12 @@
 
 namespace sscan {
 
+template <int NTL>
+__device__ __forceinline__ void zero_acc(float (&acc)[NTL][4]) {
+#pragma unroll
+    for (int j = 0; j < NTL; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+}
+
 template <typename T> struct Mma;
 
 template <> struct Mma<__nv_bfloat16> {
@@ -151,6 +157,11 @@ template <> struct Mma<float> {
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
     }
+    static __device__ __forceinline__ void mma(float (&c)[4], float (&lo)[4], const A& a, const B& b) {
+        one(lo, a.lo, b.hi);
+        one(lo, a.hi, b.lo);
+        one(c, a.hi, b.hi);
+    }
     static __device__ __forceinline__ void mma(float (&c)[4], const A& a, const B& b) {
         one(c, a.lo, b.hi);
         one(c, a.hi, b.lo);
@@ -168,6 +179,10 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[NTL][4], const T* A, int 
     typename M::Addr b_at = BT ? M::at_bt(B, pb, n0) : M::at_b(B, pb, n0);
     a_at += M::template step_k<AT>(pa) * (k_begin / M::KS);
     b_at += M::template step_k<BT>(pb) * (k_begin / M::KS);
+    // fp32: the corrections hi lo + lo hi gather apart from the products of the leading parts, which
+    // the tensor core's accumulation then truncates a third as often
+    float lo[M::kExact32 ? NTL : 1][4];
+    if constexpr (M::kExact32) zero_acc(lo);
 #pragma unroll 4
     for (int k = k_begin; k < k_end; k += M::KS) {
         typename M::A a;
@@ -176,11 +191,22 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[NTL][4], const T* A, int 
         for (int j = 0; j < NTL; j += 2) {
             typename M::B b0, b1;
             M::template fetch_b2<BT>(b0, b1, b_at + M::template step_n<BT>(pb) * (j / 2), pb);
-            M::mma(acc[j], a, b0);
-            M::mma(acc[j + 1], a, b1);
+            if constexpr (M::kExact32) {
+                M::mma(acc[j], lo[j], a, b0);
+                M::mma(acc[j + 1], lo[j + 1], a, b1);
+            } else {
+                M::mma(acc[j], a, b0);
+                M::mma(acc[j + 1], a, b1);
+            }
         }
         a_at += M::template step_k<AT>(pa);
         b_at += M::template step_k<BT>(pb);
+    }
+    if constexpr (M::kExact32) {
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] += lo[j][i];
     }
 }
 
@@ -252,12 +278,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int NTL>
-__device__ __forceinline__ void zero_acc(float (&acc)[NTL][4]) {
-#pragma unroll
-    for (int j = 0; j < NTL; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 }
 
 }  // namespace sscan
