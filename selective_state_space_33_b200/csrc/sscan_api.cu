@@ -883,14 +883,15 @@ int sscan_debug_bounds(void) {
 sscan_status sscan_device_status(int clear, unsigned int* flags) {
     g_err[0] = 0;
     if (!flags) return fail(SSCAN_ERR_INVALID_ARG, "flags is NULL");
-    unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0;
+    unsigned int f1 = 0, f2 = 0, f3 = 0, f4 = 0, f5 = 0, f6 = 0;
     cudaError_t e = sscan::read_device_error(&f1, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_bwd(&f2, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_cx(&f3, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_gated(&f4, clear);
     if (e == cudaSuccess) e = sscan::read_device_error_heads(&f5, clear);
+    if (e == cudaSuccess) e = sscan::read_device_error_walk(&f6, clear);
     if (e != cudaSuccess) return fail(SSCAN_ERR_CUDA, "reading the device error word: %s", cudaGetErrorString(e));
-    *flags = f1 | f2 | f3 | f4 | f5;
+    *flags = f1 | f2 | f3 | f4 | f5 | f6;
     return *flags ? SSCAN_ERR_TIMEOUT : SSCAN_OK;
 }
 

@@ -18,6 +18,9 @@
 #include "sscan_vec.cuh"
 
 namespace sscan {
+
+__device__ unsigned int g_device_error_walk = 0;
+
 namespace {
 
 enum { kWalkOut = 0, kWalkLocal = 1, kWalkLocalRev = 2 };
@@ -54,8 +57,24 @@ struct Walk {
         alignas(16) T sl[out && bf16 && !big ? kHeadDim * PITCH_N : 8];
         alignas(16) T fb[scale_b ? 3 : 1][scale_b ? kQ * NT : 8];  // f B in three parts
         ChunkScalars s[2];
+        unsigned int place;
     };
 };
+
+// A state handed from one segment's block to the next.
+__device__ __forceinline__ bool wait_handed(const unsigned int* p) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        unsigned int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        if (v) return true;
+        __nanosleep(64);
+    }
+    return false;
+}
+__device__ __forceinline__ void hand_on(unsigned int* p) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(1u) : "memory");
+}
+__device__ __forceinline__ void raise_heads_error() { atomicOr(&g_device_error_walk, 1u); }
 
 // barrier of the warps that run products (the scalars' warp stays out of it)
 template <int THREADS>
@@ -140,8 +159,17 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
     auto& sm = *reinterpret_cast<typename W::Smem*>(smem_raw);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int wr = w / WC, wc = w % WC;
-    const int64_t b = blockIdx.y, seg = blockIdx.x / a.H;
-    const int h = (int)(blockIdx.x - seg * a.H), grp = h / (a.H / a.G);
+    // Blocks of a split sequence run in any order; where segments hand their state on, a ticket gives
+    // them their place, segments in time order, so that the one a block waits for has started.
+    int64_t b = blockIdx.y, seg = blockIdx.x / a.H;
+    int h = (int)(blockIdx.x - seg * a.H);
+    if (MODE == kWalkOut && a.ticket) {
+        if (tid == 0) sm.place = atomicAdd(a.ticket, 1u);
+        __syncthreads();
+        const unsigned int all = (unsigned int)(a.batch * a.H), s = sm.place / all, r = sm.place - s * all;
+        seg = s, b = r / a.H, h = (int)(r - b * a.H);
+    }
+    const int grp = h / (a.H / a.G);
     const int64_t c0 = seg * a.seg_chunks, c1 = c0 + a.seg_chunks < a.chunks ? c0 + a.seg_chunks : a.chunks;
     const int64_t bh = b * a.H + h, n = c1 - c0;
     const T *u = static_cast<const T*>(kRev ? (const void*)dout : a.u), *z = static_cast<const T*>(a.z);
@@ -184,13 +212,23 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             }
     };
     if (MODE == kWalkOut) {
-        const float* first = a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N
-                             : a.h0     ? a.h0 + bh * a.P * a.N
-                                        : nullptr;
-        if (first) each_state([&](float& v, int64_t at) { v = first[at]; });
+        const bool handed = a.ticket && seg > 0;
+        const float* first = handed                   ? a.states + (bh * a.nseg + seg - 1) * a.P * a.N
+                             : a.nseg > 1 && !a.ticket ? a.states + (bh * a.nseg + seg) * a.P * a.N
+                             : a.h0                    ? a.h0 + bh * a.P * a.N
+                                                       : nullptr;
+        if (W::stages == 2) {
+            fetch(0);
+            cp_async_commit();
+        }
+        if (handed) {
+            if (tid == 0 && !wait_handed(a.handed + bh * a.nseg + seg - 1)) raise_heads_error();
+            product_sync<kWork>();
+        }
+        if (first) each_state([&](float& v, int64_t at) { v = __ldcg(first + at); });
     }
     double total = 0.0;
-    if (W::stages == 2) {
+    if (MODE != kWalkOut && W::stages == 2) {
         fetch(0);
         cp_async_commit();
     }
@@ -393,6 +431,13 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             float* o = a.h_last + bh * a.P * a.N;
             each_state([&](float& v, int64_t at) { o[at] = v; });
         }
+        if (a.ticket && seg < a.nseg - 1) {
+            float* o = a.states + (bh * a.nseg + seg) * a.P * a.N;
+            each_state([&](float& v, int64_t at) { __stcg(o + at, v); });
+            __threadfence();
+            product_sync<kWork>();
+            if (tid == 0) hand_on(a.handed + bh * a.nseg + seg);
+        }
     } else {
         float* o = a.states + (bh * a.nseg + seg) * a.P * a.N;
         each_state([&](float& v, int64_t at) { o[at] = v; });
@@ -589,14 +634,27 @@ void plan_segments(HeadsArgs& a, int64_t slots, int64_t least) {
 // Whether the tcgen05 kernel takes this problem, pointers (a.vec) aside, and its plan: one block per SM.
 bool tc_problem(const HeadsArgs& a, bool bf16) { return bf16 && a.N > 32 && a.L < (int64_t(1) << 31) - kTcQ; }
 
+// More (batch, head) pairs than the GPU holds blocks: segments of 8 chunks hand their state on, so that
+// the last wave is a few chunks long instead of a whole sequence (8 x 2048, 80 heads, 640 pairs where
+// 444 blocks fit).  With fewer pairs a block would wait for the one before it.
+constexpr int64_t kHandedChunks = 8;
+bool hands_on(const HeadsArgs& a, bool bf16) {
+    return a.batch * a.H > heads_slots(a, bf16) && a.chunks > kHandedChunks;
+}
+
 void plan_heads(HeadsArgs& a, bool bf16, bool tc) {
     if (tc) a.chunks = (a.L + kTcQ - 1) / kTcQ;
+    if (!tc && hands_on(a, bf16)) {
+        a.seg_chunks = kHandedChunks;
+        a.nseg = (a.chunks + kHandedChunks - 1) / kHandedChunks;
+        return;
+    }
     plan_segments(a, tc ? 148 : heads_slots(a, bf16), tc ? 2 : 4);
 }
 
 size_t split_bytes(const HeadsArgs& a) {
     const size_t bh = (size_t)(a.batch * a.H);
-    return round256(bh * a.nseg * a.P * a.N * sizeof(float)) + round256(bh * a.nseg * sizeof(float));
+    return round256(bh * a.nseg * a.P * a.N * sizeof(float)) + round256((bh * a.nseg + 1) * sizeof(float));
 }
 
 }  // namespace
@@ -656,6 +714,15 @@ void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, fl
     api_count_launch();
 }
 
+cudaError_t read_device_error_walk(unsigned int* value, int clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error_walk, sizeof(unsigned int));
+    if (e == cudaSuccess && clear && *value) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error_walk, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
 size_t heads_fwd_bytes(const sscan_heads_problem* p) {
     HeadsArgs a = heads_args(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
     const bool bf16 = p->io_dtype == SSCAN_BF16;
@@ -713,6 +780,13 @@ sscan_status sscan_heads_fwd(const sscan_heads_problem* p, const void* u, const 
         a.states = static_cast<float*>(workspace);
         a.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                             round256((size_t)(a.batch * a.H * a.nseg * a.P * a.N) * sizeof(float)));
+    }
+    if (a.nseg > 1 && !tc && hands_on(a, bf16)) {
+        a.ticket = reinterpret_cast<unsigned int*>(a.decays);
+        a.handed = a.ticket + 1;
+        e = cudaMemsetAsync(a.ticket, 0, (size_t)(a.batch * a.H * a.nseg + 1) * sizeof(unsigned int), st);
+        if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "clearing the segments' flags: %s", cudaGetErrorString(e));
+    } else if (a.nseg > 1) {
         e = tc ? launch_heads_tc(a, true, st) : launch_heads_local(a, nullptr, bf16, st);
         if (e != cudaSuccess) return api_fail(SSCAN_ERR_CUDA, "segment state kernel: %s", cudaGetErrorString(e));
         launch_heads_carry(a, false, h0, nullptr, st);

@@ -36,6 +36,9 @@ struct HeadsArgs {
     int64_t seg_chunks, nseg;
     float* states;            // [batch][H][nseg][P][N]: segment end states, then entering states
     float* decays;            // [batch][H][nseg]: sum of q over the segment
+    // segments handed on instead (the output pass alone): states is then the state after each, and
+    unsigned int* ticket;     // null, or the place in line of the next block
+    unsigned int* handed;     // [batch][H][nseg] 1 once that state is there
 };
 
 // Scalars of one chunk's steps, and their running sums (read two at a time, hence the alignment).

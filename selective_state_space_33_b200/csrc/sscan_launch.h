@@ -173,8 +173,10 @@ cudaError_t read_device_error(unsigned int* value, int clear);
 // carry gave up in the forward / backward kernel).  Synchronous.
 cudaError_t read_device_error_gated(unsigned int* value, int clear);
 
-// The multi-head forward's error word (bit 0: a bounded wait for a tile or a product gave up).
+// The multi-head forwards' error words (bit 0: a bounded wait for a tile, a product or an earlier
+// segment's state gave up).
 cudaError_t read_device_error_heads(unsigned int* value, int clear);
+cudaError_t read_device_error_walk(unsigned int* value, int clear);
 
 // One thread waits, with the kernels' bounded wait cut to `polls` polls, on an
 // mbarrier that nothing arrives on, then raises bit 2 of the device error word.

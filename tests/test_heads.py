@@ -101,6 +101,29 @@ def test_split_sequence(cuda_device, io):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_more_pairs_than_blocks(cuda_device, io):
+    """512 (batch, head) pairs of 1100 steps: more than the GPU holds blocks, so segments of 512 steps
+    hand their state on; twice the same bits, and a captured call replays."""
+    x = case((8, 1100, 64, 8, 4, 1), 21, io, cuda_device)
+    out, last = sb.sscan_heads_fwd(**x, return_last_state=True)
+    ref, ref_last = R.heads(**{k: R.d64(v) for k, v in x.items()})
+    assert R.off(out, ref) <= tol(out)
+    assert R.off(last, ref_last) <= (PAIR if io == "bf16" else F32)
+    again, last2 = sb.sscan_heads_fwd(**x, return_last_state=True)
+    assert torch.equal(out, again) and torch.equal(last, last2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = sb.sscan_heads_fwd(**x)
+    for _ in range(3):
+        held.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held, out)
+    assert sb.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_plain_step_sizes_and_zero_decay(cuda_device):
     """Without softplus (step sizes of either sign, growing states among them) and with A = 0,
     where the weight of the input is the step size itself."""
