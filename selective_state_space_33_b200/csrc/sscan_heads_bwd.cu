@@ -6,6 +6,7 @@
 // f_s = d_s w_s and e_t = exp(c_t):
 //   du_s = sum_t M1_ts dy_t + f_s R B_s + D dy_s
 //   dB_s = sum_t M2_ts C_t  + f_s R^T u_s        dC_t = sum_s M2_ts B_s + e_t S^T dy_t
+//     (summed over the heads of a group; they share B and C, so M2 is summed first)
 //   dz_t = dout_t y_t SiLU'(z_t),                y_t = sum_s M1_ts u_s + e_t S C_t + D u_t
 //   dc_t = sum_s G H E w_s (row t) - w_t sum_t' G H E (column t) + e_t dy_t . S C_t
 //          - w_t d_t u_t . R B_t,  and at the last step + sum_s w_s d_s u_s . R B_s + e_end R . S
@@ -15,8 +16,8 @@
 // accumulated over its heads in registers.  dA and ddelta_bias are fp32 sums over the whole
 // sequence of differences that nearly cancel (with two bf16 parts, 16 bits, a bias gradient came out
 // 8e-5 off where the same sums in fp32 lose 1e-6), so everything that feeds them (H, S C, R B)
-// takes its inexact factor as three bf16 parts, 24 bits; M1, M2 and the factors of the
-// products that end in bf16 are rounded once.
+// takes its inexact factor as three bf16 parts, 24 bits; M1 and the factors of the products
+// that end in bf16 are rounded once.
 #include <cuda_runtime.h>
 
 #include "sscan_heads.cuh"
@@ -54,7 +55,7 @@ struct BwdSmem {
     alignas(16) T sl[two ? kHeadDim * Pt::N : 1];
     alignas(16) T rh[kHeadDim * Pt::N];          // R, [p][n]
     alignas(16) T rl[two ? kHeadDim * Pt::N : 1];
-    // M1 and M2, [t][s]; before them, in bf16, the third parts of R and S, and then of dy
+    // M1, and at the end M2, [t][s]; before them, in bf16, the third parts of R and S, and then of dy
     static constexpr int M = two && Pt::N > Pt::Q ? kHeadDim * Pt::N : kQ * Pt::Q;
     alignas(16) T m1[M];
     alignas(16) T m2[M];
@@ -149,6 +150,8 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
     if (lower) warp_gemm<T, false, false, 4>(G, sm.C, Pt::N, 16 * wr, sm.B, Pt::N, 32 * wc, 0, NT);
     float bc[NTL][4];                                     // wc = 0: dC (rows t), wc = 1: dB (rows s)
     zero_acc(bc);
+    float M2[4][4];                                       // sum of M2 over the heads, which share B and C
+    zero_acc(M2);
 
     for (int h = h_begin; h < h_end; ++h) {
         const int64_t bh = b * a.H + h;
@@ -280,36 +283,6 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             va = quad_sum(va);
             vb = quad_sum(vb);
             if (q == 0) sm.rs[wc][ra] = va, sm.rs[wc][rb] = vb;
-            zero_acc(y);
-            warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
-            if constexpr (!M::kExact32) {
-                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sl, Pt::N, 32 * wc, 0, NT);
-                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.m2, Pt::N, 32 * wc, 0, NT);
-            }
-            const float ea = sm.s.e[ra], eb = sm.s.e[rb];
-            va = vb = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const int at = (i ? rb : ra) * Pt::P + cb + 8 * j;
-                    float dy[2];
-                    load_shared<2>(sm.dyh + at, dy);
-                    if constexpr (!M::kExact32) {
-                        float lo[2];
-                        load_shared<2>(sm.dyl + at, lo);
-                        dy[0] += lo[0], dy[1] += lo[1];
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        y[j][i + n] *= i ? eb : ea;
-                        (i ? vb : va) += y[j][i + n] * dy[n];
-                        x[j][i + n] = fmaf(D, dy[n], x[j][i + n]);
-                    }
-                }
-            va = quad_sum(va);
-            vb = quad_sum(vb);
-            if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
         }
         if (!M::kExact32 && z) {
             // the third part of dy takes the place of R's
@@ -322,6 +295,42 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                 }
             }
             __syncthreads();
+        }
+        {
+            zero_acc(y);
+            warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
+            if constexpr (!M::kExact32) {
+                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sl, Pt::N, 32 * wc, 0, NT);
+                warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.m2, Pt::N, 32 * wc, 0, NT);
+            }
+            const float ea = sm.s.e[ra], eb = sm.s.e[rb];
+            float va = 0.f, vb = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const int at = (i ? rb : ra) * Pt::P + cb + 8 * j;
+                    float dy[2];
+                    load_shared<2>(sm.dyh + at, dy);
+                    if constexpr (!M::kExact32) {
+                        float lo[2];
+                        load_shared<2>(sm.dyl + at, lo);
+                        dy[0] += lo[0], dy[1] += lo[1];
+                        if (z) {
+                            load_shared<2>(sm.m1 + at, lo);
+                            dy[0] += lo[0], dy[1] += lo[1];
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        y[j][i + n] *= i ? eb : ea;
+                        (i ? vb : va) += y[j][i + n] * dy[n];
+                        x[j][i + n] = fmaf(D, dy[n], x[j][i + n]);
+                    }
+                }
+            va = quad_sum(va);
+            vb = quad_sum(vb);
+            if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
         }
         // H, then M1, M2 and the sums of G H E over rows and columns
         float Hm[4][4];
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
                 const int t = i ? rb : ra;
-                float m1[2], m2[2];
+                float m1[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const float E = ex2(((i ? chb : cha) - (n ? chs.y : chs.x)) + ((i ? clb : cla) - (n ? cls.y : cls.x)));
@@ -357,10 +366,9 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                     cols[n] += pair;
                     (i ? rowb : rowa) += pair * w_;
                     m1[n] = ge * w_;
-                    m2[n] = he * w_;
+                    M2[j][i + n] = fmaf(he, w_, M2[j][i + n]);
                 }
                 store_vec<2>(sm.m1 + t * Pt::Q + s0, m1);
-                store_vec<2>(sm.m2 + t * Pt::Q + s0, m2);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -425,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             float v[HTL][4];
             zero_acc(v);
             if (wc == 0) warp_gemm<T, false, true, HTL>(v, sm.dyh, Pt::P, 16 * wr, sm.sh, Pt::N, 8 * n0, 0, kHeadDim);
-            // with a gate dy is not exact either: the second part of S keeps dC to two roundings, as dB
+            // with a gate dy is rounded too: the second part of S keeps dC to one more rounding, as dB
             if (!M::kExact32 && z && wc == 0)
                 warp_gemm<T, false, true, HTL>(v, sm.dyh, Pt::P, 16 * wr, sm.sl, Pt::N, 8 * n0, 0, kHeadDim);
             if (wc != 0) warp_gemm<T, false, true, HTL>(v, sm.x, Pt::P, 16 * wr, sm.rh, Pt::N, 8 * n0, 0, kHeadDim);
@@ -435,8 +443,6 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                 v[j][0] *= fa, v[j][1] *= fa;
                 v[j][2] *= fb, v[j][3] *= fb;
             }
-            if (wc == 0) warp_gemm<T, false, true, HTL>(v, sm.m2, Pt::Q, 16 * wr, sm.B, Pt::N, 8 * n0, 0, 16 * wr + 16);
-            else warp_gemm<T, true, true, HTL>(v, sm.m2, Pt::Q, 16 * wr, sm.C, Pt::N, 8 * n0, 16 * wr, kQ);
 #pragma unroll
             for (int j = 0; j < HTL; ++j)
 #pragma unroll
@@ -495,6 +501,19 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
         }
         __syncthreads();
     }
+    // M2 B and M2^T C, once for all heads, M2 in two parts
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        split_store2<T>(sm.m1, sm.m2, ra * Pt::Q + cb + 8 * j, M2[j][0], M2[j][1]);
+        split_store2<T>(sm.m1, sm.m2, rb * Pt::Q + cb + 8 * j, M2[j][2], M2[j][3]);
+    }
+    __syncthreads();
+    auto through_m2 = [&](const T* m) {
+        if (wc == 0) warp_gemm<T, false, true, NTL>(bc, m, Pt::Q, 16 * wr, sm.B, Pt::N, 0, 0, 16 * wr + 16);
+        else warp_gemm<T, true, true, NTL>(bc, m, Pt::Q, 16 * wr, sm.C, Pt::N, 0, 16 * wr, kQ);
+    };
+    through_m2(sm.m1);
+    if constexpr (!M::kExact32) through_m2(sm.m2);
     // dC or dB over this block's heads
 #pragma unroll
     for (int j = 0; j < NTL; ++j)
