@@ -703,8 +703,8 @@ def sscan_heads_step(u, delta_raw, A, B, C, state, delta_bias=None, D_skip=None,
 
 def device_status(clear: bool = False) -> int:
     """Error bits the library's kernels raised on the current device since the last
-    clear (0: none; bit 0 forward, bit 1 backward: a bounded wait for a tile copy gave
-    up; bit 2: the wait-timeout probe).  Synchronous."""
+    clear (0: none; bit 0 forward, bit 1 backward: a bounded wait for a tile copy, a product or
+    an earlier tile's carry gave up; bit 2: the wait-timeout probe).  Synchronous."""
     lib = load_library()
     flags = ctypes.c_uint(0)
     st = lib.sscan_device_status(int(clear), ctypes.byref(flags))

@@ -101,11 +101,12 @@ def test_split_sequence(cuda_device, io):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("io", ["f32", "bf16"])
-def test_more_pairs_than_blocks(cuda_device, io):
-    """512 (batch, head) pairs of 1100 steps: more than the GPU holds blocks, so segments of 512 steps
-    hand their state on; twice the same bits, and a captured call replays."""
-    x = case((8, 1100, 64, 8, 4, 1), 21, io, cuda_device)
+@pytest.mark.parametrize("io,shape", [("f32", (8, 1100, 64, 8, 4, 1)), ("bf16", (8, 1100, 64, 8, 4, 1)),
+                                      ("f32", (4, 600, 40, 8, 80, 1)), ("bf16", (8, 600, 60, 9, 40, 2))])
+def test_more_pairs_than_blocks(cuda_device, io, shape):
+    """More (batch, head) pairs than the GPU holds blocks: segments of 512 steps hand their state on;
+    twice the same bits, and a captured call replays."""
+    x = case(shape, 21, io, cuda_device)
     out, last = sb.sscan_heads_fwd(**x, return_last_state=True)
     ref, ref_last = R.heads(**{k: R.d64(v) for k, v in x.items()})
     assert R.off(out, ref) <= tol(out)
