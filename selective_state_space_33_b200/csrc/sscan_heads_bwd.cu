@@ -55,7 +55,8 @@ struct BwdSmem {
     alignas(16) T sl[two ? kHeadDim * Pt::N : 1];
     alignas(16) T rh[kHeadDim * Pt::N];          // R, [p][n]
     alignas(16) T rl[two ? kHeadDim * Pt::N : 1];
-    // M1, and at the end M2, [t][s]; before them, in bf16, the third parts of R and S, and then of dy
+    alignas(16) T dy3[two ? kQ * Pt::P : 8];     // third part of dy
+    // M1, and at the end M2, [t][s]; before them, in bf16, the third parts of R and S
     static constexpr int M = two && Pt::N > Pt::Q ? kHeadDim * Pt::N : kQ * Pt::Q;
     alignas(16) T m1[M];
     alignas(16) T m2[M];
@@ -160,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
         // u, dy and their product's sum
         float dsum = 0.f, ssum = 0.f;
         constexpr int VE = 16 / sizeof(T), PER = kHeadDim / VE, LOADS = kQ * PER / kThreads;
-        uint32_t dy3[M::kExact32 ? 1 : LOADS][VE / 2];   // third parts of dy, for later
         {
 #pragma unroll
             for (int n = 0; n < LOADS; ++n) {
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                     if (z) dv[j] *= silu(zv[j]), dv[j + 1] *= silu(zv[j + 1]);
                     dsum = fmaf(dv[j], xv[j], fmaf(dv[j + 1], xv[j + 1], dsum));
                     const uint32_t third = split_store2<T>(sm.dyh, sm.dyl, t * Pt::P + p + j, dv[j], dv[j + 1]);
-                    if constexpr (!M::kExact32) dy3[n][j / 2] = third;
+                    if constexpr (!M::kExact32) *reinterpret_cast<uint32_t*>(sm.dy3 + t * Pt::P + p + j) = third;
                 }
                 store_vec<VE>(sm.x + t * Pt::P + p, xv);
             }
@@ -258,6 +258,55 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             }
         };
 
+        // H, M1 and M2, and the sums of G H E over rows and columns
+        Vec<T, 2> m1v[4][2];
+        float Hm[4][4];
+        zero_acc(Hm);
+        if (lower) {
+            warp_gemm<T, false, false, 4>(Hm, sm.dyh, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
+            if (!M::kExact32 && z) {
+                warp_gemm<T, false, false, 4>(Hm, sm.dyl, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
+                warp_gemm<T, false, false, 4>(Hm, sm.dy3, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
+            }
+        }
+        float rowa = 0.f, rowb = 0.f;
+        const float cha = sm.s.ch[ra], cla = sm.s.cl[ra], chb = sm.s.ch[rb], clb = sm.s.cl[rb];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s0 = cb + 8 * j;
+            const float2 ws = *reinterpret_cast<const float2*>(sm.s.w + s0);
+            const float2 chs = *reinterpret_cast<const float2*>(sm.s.ch + s0);
+            const float2 cls = *reinterpret_cast<const float2*>(sm.s.cl + s0);
+            float cols[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const int t = i ? rb : ra;
+                float m1[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float E = ex2(((i ? chb : cha) - (n ? chs.y : chs.x)) + ((i ? clb : cla) - (n ? cls.y : cls.x)));
+                    const float w_ = n ? ws.y : ws.x;
+                    const bool in = s0 + n <= t;
+                    const float ge = in ? G[j][i + n] * E : 0.f, he = in ? Hm[j][i + n] * E : 0.f;
+                    const float pair = in ? ge * Hm[j][i + n] : 0.f;
+                    cols[n] += pair;
+                    (i ? rowb : rowa) += pair * w_;
+                    m1[n] = ge * w_;
+                    M2[j][i + n] = fmaf(he, w_, M2[j][i + n]);
+                }
+                m1v[j][i / 2].set(m1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v = cols[i];
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (g == 0) sm.col[wr][s0 + i] = v;
+            }
+        }
+        rowa = quad_sum(rowa);
+        rowb = quad_sum(rowb);
+        if (q == 0) sm.row[wc][ra] = rowa, sm.row[wc][rb] = rowb;
         // R B (rows s, columns p) and S C (rows t, columns p): both end in fp32 sums over the sequence
         // that nearly cancel, so R, S and dy enter with 24 bits
         float x[4][4], y[4][4];
@@ -284,18 +333,6 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             vb = quad_sum(vb);
             if (q == 0) sm.rs[wc][ra] = va, sm.rs[wc][rb] = vb;
         }
-        if (!M::kExact32 && z) {
-            // the third part of dy takes the place of R's
-            __syncthreads();
-            if constexpr (!M::kExact32) {
-#pragma unroll
-                for (int n = 0; n < LOADS; ++n) {
-                    const int i = tid + n * kThreads, t = i / PER, p = (i - t * PER) * VE;
-                    *reinterpret_cast<uint4*>(sm.m1 + t * Pt::P + p) = make_uint4(dy3[n][0], dy3[n][1], dy3[n][2], dy3[n][3]);
-                }
-            }
-            __syncthreads();
-        }
         {
             zero_acc(y);
             warp_gemm<T, false, false, 4>(y, sm.C, Pt::N, 16 * wr, sm.sh, Pt::N, 32 * wc, 0, NT);
@@ -317,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
                         load_shared<2>(sm.dyl + at, lo);
                         dy[0] += lo[0], dy[1] += lo[1];
                         if (z) {
-                            load_shared<2>(sm.m1 + at, lo);
+                            load_shared<2>(sm.dy3 + at, lo);
                             dy[0] += lo[0], dy[1] += lo[1];
                         }
                     }
@@ -332,55 +369,12 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             vb = quad_sum(vb);
             if (q == 0) sm.qs[wc][ra] = va, sm.qs[wc][rb] = vb;
         }
-        // H, then M1, M2 and the sums of G H E over rows and columns
-        float Hm[4][4];
-        zero_acc(Hm);
-        if (lower) {
-            warp_gemm<T, false, false, 4>(Hm, sm.dyh, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
-            if (!M::kExact32 && z) {
-                warp_gemm<T, false, false, 4>(Hm, sm.dyl, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
-                warp_gemm<T, false, false, 4>(Hm, sm.m1, Pt::P, 16 * wr, sm.x, Pt::P, 32 * wc, 0, kHeadDim);
-            }
-        }
-        if constexpr (!M::kExact32) __syncthreads();  // the third parts are read
-        float rowa = 0.f, rowb = 0.f;
-        const float cha = sm.s.ch[ra], cla = sm.s.cl[ra], chb = sm.s.ch[rb], clb = sm.s.cl[rb];
+        if constexpr (!M::kExact32) __syncthreads();  // the third parts, whose place M1 takes, are read
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int s0 = cb + 8 * j;
-            const float2 ws = *reinterpret_cast<const float2*>(sm.s.w + s0);
-            const float2 chs = *reinterpret_cast<const float2*>(sm.s.ch + s0);
-            const float2 cls = *reinterpret_cast<const float2*>(sm.s.cl + s0);
-            float cols[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const int t = i ? rb : ra;
-                float m1[2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float E = ex2(((i ? chb : cha) - (n ? chs.y : chs.x)) + ((i ? clb : cla) - (n ? cls.y : cls.x)));
-                    const float w_ = n ? ws.y : ws.x;
-                    const bool in = s0 + n <= t;
-                    const float ge = in ? G[j][i + n] * E : 0.f, he = in ? Hm[j][i + n] * E : 0.f;
-                    const float pair = in ? ge * Hm[j][i + n] : 0.f;
-                    cols[n] += pair;
-                    (i ? rowb : rowa) += pair * w_;
-                    m1[n] = ge * w_;
-                    M2[j][i + n] = fmaf(he, w_, M2[j][i + n]);
-                }
-                store_vec<2>(sm.m1 + t * Pt::Q + s0, m1);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v = cols[i];
-#pragma unroll
-                for (int o = 4; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (g == 0) sm.col[wr][s0 + i] = v;
-            }
+            m1v[j][0].store(sm.m1 + ra * Pt::Q + cb + 8 * j);
+            m1v[j][1].store(sm.m1 + rb * Pt::Q + cb + 8 * j);
         }
-        rowa = quad_sum(rowa);
-        rowb = quad_sum(rowb);
-        if (q == 0) sm.row[wc][ra] = rowa, sm.row[wc][rb] = rowb;
         __syncthreads();
 
         // du, and with a gate dz
@@ -556,6 +550,7 @@ cudaError_t bwd(const HeadsBwdArgs& k, cudaStream_t st) {
     auto* fn = heads_bwd_kernel<T, NT>;
     constexpr size_t smem = sizeof(BwdSmem<T, NT>);
     static_assert(smem <= 227 * 1024, "the tiles of one chunk must fit a block's shared memory");
+    static_assert(sizeof(T) == 4 || NT > 64 || 2 * (smem + 1024) <= 228 * 1024, "two blocks per SM up to 64 states");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     fn<<<dim3((unsigned)k.f.chunks, (unsigned)k.f.batch, (unsigned)(k.f.G * k.splits)), kThreads, smem, st>>>(k);
