@@ -15,7 +15,7 @@
 //   St = B^T (f U)     rows n, columns p   (B [s][n], f U [s][p], both MN-major)           64
 // y = exp(c) Ya + Yb.  f U goes in as three bf16 parts (24 bits: the state is an fp32 result), S and M
 // as one, each a rounding of the size of the output's own.  The state itself stays in fp32
-// registers, row n and half of the channels per thread.
+// registers, row n and a quarter of the channels per thread.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -33,7 +33,8 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kWork = 256;               // 8 warps: 4 quarters of the rows by 2 halves of the columns
+constexpr int kWork = 512;               // 16 warps: 4 quarters of the rows by 4 of the columns
+constexpr int kIssuer = kWork / 32;      // index of the issuing warp
 constexpr int kIssue = kWork + 32;       // and the warp that issues products and copies
 constexpr int kThreads = kIssue + 64;    // and one each for the scalars of even and odd chunks
 constexpr int kTile = kTcQ * 64;         // elements of a tile of 128 rows
@@ -84,7 +85,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 rows.
+// 32 or 16 columns of this warp's 32 rows.
 __device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
     uint32_t r[32];
     asm volatile(
@@ -99,6 +100,18 @@ __device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t at) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
@@ -201,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(&g_device_error_heads, 1u);
     };
 
-    if (w > 8) {
+    if (w > kIssuer) {
         // the scalars, up to four chunks ahead: a long chain of dependent operations (fp64 sums)
-        for (int i = w - 9; i < n; i += 2) {
+        for (int i = w - kIssuer - 1; i < n; i += 2) {
             if (i > 3) wait(&sm.scalars_free[i & 3], (i - 4) >> 2);
             chunk_scalars<bf16, kTcQ>(sm.s[i & 3], a, b, h, (c0 + i) * kTcQ);
             __syncwarp();
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         return;
     }
-    if (w == 8) {
+    if (w == kIssuer) {
         // one lane issues; the warp keeps the barriers
         const bool one = lane == 0;
         auto at = [&](int i) { return (int)((c0 + i) * kTcQ); };
@@ -298,26 +311,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
-    const int quarter = w & 3, half = w >> 2, r = 32 * quarter + lane;   // this thread's row and half of the columns
+    const int quarter = w & 3, part4 = w >> 2, r = 32 * quarter + lane;  // this thread's row and quarter of the columns
+    const int p0 = 16 * part4;
     const uint32_t tm_row = tmem + ((uint32_t)(32 * quarter) << 16);
-    // the state: row n = r, channels 32 half .. + 31
-    float S[32];
+    // the state: row n = r, channels p0 .. p0 + 15
+    float S[16];
     {
         const float* first = !kOut ? nullptr : a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N : a.h0 ? a.h0 + bh * a.P * a.N : nullptr;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const int p = 32 * half + k;
+        for (int k = 0; k < 16; ++k) {
+            const int p = p0 + k;
             S[k] = first && r < a.N && p < a.P ? first[(int64_t)p * a.N + r] : 0.f;
         }
     }
     auto put_state = [&] {  // bf16 S for Ya: row r of [n][p]
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             uint4 v;
             uint32_t* o = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = Mma<bf16>::pack(S[8 * k + 2 * i], S[8 * k + 2 * i + 1]);
-            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.S) + unit(r, 4 * half + k)) = v;
+            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(sm.S) + unit(r, 2 * part4 + k)) = v;
         }
     };
     if (kOut) {
@@ -338,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float probe = 0.f;
         unsigned char* xb = reinterpret_cast<unsigned char*>(sm.x[buf]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = (tid >> 3) + 32 * k;
+        for (int k = 0; k < 2; ++k) {
+            const int row = (tid >> 3) + 64 * k;
             const uint32_t at = unit(row, tid & 7);
             float v[8];
             widen8(*reinterpret_cast<const uint4*>(xb + at), v);
@@ -369,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kOut && bad) {
             // Such a value would meet the zeros of M above the diagonal: it is left out of the product
             // and its terms are added to the steps that have them, below.
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t at = unit((tid >> 3) + 32 * k, tid & 7);
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t at = unit((tid >> 3) + 64 * k, tid & 7);
                 uint32_t* v = reinterpret_cast<uint32_t*>(xb + at);
                 for (int e = 0; e < 4; ++e) {
                     if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u;
@@ -380,36 +394,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async();
         }
         if (kOut) {
-            // M: row t = r, columns s = 64 half .. + 63
+            // M: row t = r, columns s = 32 part4 .. + 31
             wait(&sm.done_g, i);
             fence_after();
             const float ch = sc.ch[r], cl = sc.cl[r];
+            const int s0 = 32 * part4;
+            uint32_t m[16];
+            if (part4 > quarter) {                     // all above the diagonal
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int s0 = 64 * half + 32 * g;
-                uint32_t m[16];
-                if (s0 > 32 * quarter + 31) {          // all above the diagonal
+                for (int k = 0; k < 16; ++k) m[k] = 0u;
+            } else {
+                float v[32];
+                tmem_load(v, tm_row + kColG + s0);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) m[k] = 0u;
-                } else {
-                    float v[32];
-                    tmem_load(v, tm_row + kColG + s0);
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 chs = *reinterpret_cast<const float4*>(sc.ch + s0 + k);
+                    const float4 cls = *reinterpret_cast<const float4*>(sc.cl + s0 + k);
+                    const float4 ws = *reinterpret_cast<const float4*>(sc.w + s0 + k);
+                    const float cs[4] = {chs.x, chs.y, chs.z, chs.w}, ls[4] = {cls.x, cls.y, cls.z, cls.w},
+                                wv[4] = {ws.x, ws.y, ws.z, ws.w};
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 chs = *reinterpret_cast<const float4*>(sc.ch + s0 + k);
-                        const float4 cls = *reinterpret_cast<const float4*>(sc.cl + s0 + k);
-                        const float4 ws = *reinterpret_cast<const float4*>(sc.w + s0 + k);
-                        const float cs[4] = {chs.x, chs.y, chs.z, chs.w}, ls[4] = {cls.x, cls.y, cls.z, cls.w},
-                                    wv[4] = {ws.x, ws.y, ws.z, ws.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[k + e] = s0 + k + e <= r ? v[k + e] * (ex2((ch - cs[e]) + (cl - ls[e])) * wv[e]) : 0.f;
-                        m[k / 2] = Mma<bf16>::pack(v[k], v[k + 1]);
-                        m[k / 2 + 1] = Mma<bf16>::pack(v[k + 2], v[k + 3]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        v[k + e] = s0 + k + e <= r ? v[k + e] * (ex2((ch - cs[e]) + (cl - ls[e])) * wv[e]) : 0.f;
+                    m[k / 2] = Mma<bf16>::pack(v[k], v[k + 1]);
+                    m[k / 2 + 1] = Mma<bf16>::pack(v[k + 2], v[k + 3]);
                 }
-                tmem_store16(tm_row + kColM + s0 / 2, m);
             }
+            tmem_store16(tm_row + kColM + s0 / 2, m);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             work_sync();
@@ -421,26 +432,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             const float dec = ex2(sc.total * kLog2e);
             total += sc.total;
-            float v[32];
-            tmem_load(v, tm_row + kColSt + 32 * half);
+            float v[16];
+            tmem_load(v, tm_row + kColSt + p0);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) S[k] = fmaf(dec, S[k], v[k]);
+            for (int k = 0; k < 16; ++k) S[k] = fmaf(dec, S[k], v[k]);
         }
         if (kOut) {
             put_state();
             wait(&sm.done_yb, i);
             wait(&sm.full_z, i);
             fence_after();
-            float ya[32], yb[32];
-            tmem_load(ya, tm_row + kColYa + 32 * half);
-            tmem_load(yb, tm_row + kColYb + 32 * half);
+            float ya[16], yb[16];
+            tmem_load(ya, tm_row + kColYa + p0);
+            tmem_load(yb, tm_row + kColYb + p0);
             const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
             unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z);
             // written twice: the calls of the rare form would cost the usual one its registers
             auto outputs = [&](auto rare) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t at = unit(r, 4 * half + k);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t at = unit(r, 2 * part4 + k);
                     float xv[8], zv[8], y[8];
                     widen8(*reinterpret_cast<const uint4*>(xb + at), xv);
                     if (gate) widen8(*reinterpret_cast<const uint4*>(zb + at), zv);
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 8; ++j) {
                         y[j] = fmaf(e, ya[8 * k + j], yb[8 * k + j]);
                         if constexpr (decltype(rare)::value) {
-                            const int p = 32 * half + 8 * k + j;
+                            const int p = p0 + 8 * k + j;
                             if (t0 + r < a.L && p < a.P) {
                                 y[j] += not_finite_terms(a, sc, b, h, grp, t0, r, p);
                                 xv[j] = __bfloat162float(static_cast<const bf16*>(a.u)[((b * a.L + t0 + r) * a.H + h) * a.P + p]);
@@ -472,15 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kOut) {
         if (a.h_last && seg == a.nseg - 1 && r < a.N) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (32 * half + k < a.P) a.h_last[bh * a.P * a.N + (int64_t)(32 * half + k) * a.N + r] = S[k];
+            for (int k = 0; k < 16; ++k)
+                if (p0 + k < a.P) a.h_last[bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
         }
         work_sync();                           // the last chunk's outputs may leave
     } else {
         if (r < a.N) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (32 * half + k < a.P) a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(32 * half + k) * a.N + r] = S[k];
+            for (int k = 0; k < 16; ++k)
+                if (p0 + k < a.P) a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
         }
         if (tid == 0) a.decays[bh * a.nseg + seg] = (float)total;
     }
