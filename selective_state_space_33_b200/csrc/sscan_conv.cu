@@ -71,7 +71,8 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t d, float (&
 }
 
 // One thread: V channels of one batch row, `tile` steps.  Threads run along the channels
-// first, so that a warp's accesses are consecutive.
+// first, so that a warp's accesses are consecutive.  8 x 2048 x 1536 bf16, 4 taps, SiLU: 25-26 us,
+// 4.0 TB/s; what is left over the 15.4 us of its bytes is the latency of one wave of threads.
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(128, 8) conv_fwd_kernel(ConvArgs a) {
     const int64_t cols = a.D / V;
@@ -138,7 +139,8 @@ constexpr int kBwdGroups = 8;  // stretches per block, whose dW partials the blo
 // dy_t = dout_t act'(y_t);  dx_t = sum_k W[k] dy_{t+K-1-k};  dW[k] = sum_t dy_t x_{t-K+1+k}.
 // A block is 32 lanes of V channels by kBwdGroups stretches of `tile` steps; each thread runs
 // K-1 steps past its stretch to have every dy its dx needs (recomputed, not exchanged: two
-// rows in `tile`), and the block writes one row of dW and dbias partial sums.
+// rows in `tile`), and the block writes one row of dW and dbias partial sums.  3 x 1021 x 1531 fp32
+// (an odd width: one channel per thread): 21 us, 2.7 TB/s.
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a) {
     __shared__ float red[kBwdGroups][(K + 1) * V][33];
@@ -256,7 +258,9 @@ __global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a
     }
 }
 
-// One token: the window is the state; shift it in place.
+// One token: the window is the state; shift it in place.  64 x 5120 bf16, 4 taps: 3.6 us for 5 MB,
+// a launch's own latency; two channels per thread, since wider ones leave too few threads (9.7 us
+// at eight).
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
     const int64_t cols = a.D / V;

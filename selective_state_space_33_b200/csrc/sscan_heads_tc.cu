@@ -4,7 +4,11 @@
 // With 128 states the chunk's products are 2 x 128 x (128 + 3 x 64 + 64 + 64) x 128 operations against 48 KB
 // of traffic; as mma.sync they kept eight warps loading fragments (1470 us at 65536 steps, 24 heads, 128
 // states, issue slots 45% busy, tensor pipe under 40%).  Here one thread issues them from
-// shared memory and tensor memory, and the warps only do what is elementwise.
+// shared memory and tensor memory, and the warps only do what is elementwise: 640 us, of which the
+// output pass 460 and the pass over the segments' states 175.  What is left is the order of a chunk's
+// steps with one block per SM (issue slots 32%, tensor pipe 17% busy); barriers that keep the
+// working warps in step are faster than mbarriers that let them drift (815 against 764 us at
+// that stage: drifting warps miss the instruction cache).
 //
 // A block walks the chunks (128 steps) of one (batch, head, segment).  Tiles are rows of 64 bf16 in the
 // 128-byte swizzle, as TMA writes them: such a tile is a K-major operand when its rows are
@@ -19,8 +23,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
-
-#include <type_traits>
 
 #include "sscan_heads.cuh"
 #include "sscan_vec.cuh"
@@ -160,21 +162,38 @@ __device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 
-// The terms M_ts u_s, s <= t, of one channel whose u_s is not finite, from global memory.
-__device__ __noinline__ float not_finite_terms(const HeadsArgs& a, const ChunkScalarsOf<kTcQ>& s, int64_t b, int h, int grp,
-                                               int64_t t0, int t, int p) {
+// The outputs of a thread's 16 channels at step t of a chunk with values of u that are not finite: such
+// values were left out of Yb, and the terms M_ts u_s that hold one are added for s <= t alone, from
+// global memory.  A function of its own: inlined, its registers cost the usual path a tenth of its time.
+__device__ __noinline__ void rare_outputs(const HeadsArgs& a, const ChunkScalarsOf<kTcQ>& s, uint32_t ya_at, uint32_t yb_at,
+                                          unsigned char* zb, int b, int h, int64_t t0, int t, int p0) {
     const bf16 *u = static_cast<const bf16*>(a.u), *B = static_cast<const bf16*>(a.B), *C = static_cast<const bf16*>(a.C);
-    float v = 0.f;
-    for (int q = 0; q <= t; ++q) {
-        const float x = __bfloat162float(u[((b * a.L + t0 + q) * a.H + h) * a.P + p]);
-        if (fabsf(x) <= 3.4e38f) continue;
-        float dot = 0.f;
-        for (int n = 0; n < a.N; ++n)
-            dot = fmaf(__bfloat162float(C[((b * a.L + t0 + t) * a.G + grp) * a.N + n]),
-                       __bfloat162float(B[((b * a.L + t0 + q) * a.G + grp) * a.N + n]), dot);
-        v += dot * (chunk_decay(s, t, q) * s.w[q]) * x;
+    const int grp = h / (a.H / a.G);
+    const float e = s.e[t], D = a.D ? __ldg(a.D + h) : 0.f;
+    float ya[16], yb[16];
+    tmem_load(ya, ya_at);
+    tmem_load(yb, yb_at);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int p = p0 + j;
+        bf16* z = reinterpret_cast<bf16*>(zb + unit(t, p / 8)) + p % 8;
+        float v = fmaf(e, ya[j], yb[j]), x = 0.f;
+        if (t0 + t < a.L && p < a.P) {
+            x = __bfloat162float(u[((b * a.L + t0 + t) * a.H + h) * a.P + p]);
+            for (int q = 0; q <= t; ++q) {
+                const float uq = __bfloat162float(u[((b * a.L + t0 + q) * a.H + h) * a.P + p]);
+                if (fabsf(uq) <= 3.4e38f) continue;
+                float dot = 0.f;
+                for (int n = 0; n < a.N; ++n)
+                    dot = fmaf(__bfloat162float(C[((b * a.L + t0 + t) * a.G + grp) * a.N + n]),
+                               __bfloat162float(B[((b * a.L + t0 + q) * a.G + grp) * a.N + n]), dot);
+                v += dot * (chunk_decay(s, t, q) * s.w[q]) * uq;
+            }
+        }
+        if (a.D) v = fmaf(D, x, v);
+        if (a.z) v *= silu(__bfloat162float(*z));
+        *z = __float2bfloat16_rn(v);
     }
-    return v;
 }
 
 // kOut: outputs, from the state entering the segment; else the segment's end state from zero.
@@ -182,7 +201,7 @@ template <int NT, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     heads_tc_kernel(const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_z,
                     const __grid_constant__ CUtensorMap tm_B, const __grid_constant__ CUtensorMap tm_C,
-                    const __grid_constant__ CUtensorMap tm_out, HeadsArgs a) {
+                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ HeadsArgs a) {
     constexpr int HALVES = NT / 64;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     auto& sm = *reinterpret_cast<TcSmem*>(smem_raw);
@@ -442,13 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&sm.done_yb, i);
             wait(&sm.full_z, i);
             fence_after();
-            float ya[16], yb[16];
-            tmem_load(ya, tm_row + kColYa + p0);
-            tmem_load(yb, tm_row + kColYb + p0);
-            const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
-            unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z);
-            // written twice: the calls of the rare form would cost the usual one its registers
-            auto outputs = [&](auto rare) {
+            if (bad) {
+                rare_outputs(a, sc, tm_row + kColYa + p0, tm_row + kColYb + p0, reinterpret_cast<unsigned char*>(sm.z), b, h, t0, r, p0);
+            } else {
+                float ya[16], yb[16];
+                tmem_load(ya, tm_row + kColYa + p0);
+                tmem_load(yb, tm_row + kColYb + p0);
+                const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
+                unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t at = unit(r, 2 * part4 + k);
@@ -458,13 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         y[j] = fmaf(e, ya[8 * k + j], yb[8 * k + j]);
-                        if constexpr (decltype(rare)::value) {
-                            const int p = p0 + 8 * k + j;
-                            if (t0 + r < a.L && p < a.P) {
-                                y[j] += not_finite_terms(a, sc, b, h, grp, t0, r, p);
-                                xv[j] = __bfloat162float(static_cast<const bf16*>(a.u)[((b * a.L + t0 + r) * a.H + h) * a.P + p]);
-                            }
-                        }
                         if (a.D) y[j] = fmaf(D, xv[j], y[j]);
                         if (gate) y[j] *= silu(zv[j]);
                     }
@@ -474,9 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j) ow[j] = Mma<bf16>::pack(y[2 * j], y[2 * j + 1]);
                     *reinterpret_cast<uint4*>(zb + at) = o;
                 }
-            };
-            if (bad) outputs(std::true_type{});
-            else outputs(std::false_type{});
+            }
             fence_proxy_async();
         }
     }
