@@ -71,7 +71,7 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t d, float (&
 }
 
 // One thread: V channels of one batch row, `tile` steps.  Threads run along the channels
-// first, so that a warp's accesses are consecutive.  8 x 2048 x 1536 bf16, 4 taps, SiLU: 25-26 us,
+// first, so that a warp's accesses are consecutive.  8 x 2048 x 1536 bf16, 4 taps, SiLU: 25 us,
 // 4.0 TB/s; what is left over the 15.4 us of its bytes is the latency of one wave of threads.
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(128, 8) conv_fwd_kernel(ConvArgs a) {
@@ -258,9 +258,8 @@ __global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a
     }
 }
 
-// One token: the window is the state; shift it in place.  64 x 5120 bf16, 4 taps: 3.6 us for 5 MB,
-// a launch's own latency; two channels per thread, since wider ones leave too few threads (9.7 us
-// at eight).
+// One token: the window is the state; shift it in place.  64 x 5120 bf16, 4 taps: 2.8-3.5 us for 5 MB
+// as a graph's node, a launch's own latency; two channels per thread (four 3.5-4.2 us, one 3.5).
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
     const int64_t cols = a.D / V;

@@ -24,8 +24,8 @@
 // flag: the arrays start as all ones, a NaN that no arithmetic returns, and each 8-byte word is
 // stored and polled whole, so no fence or second round trip is needed.
 //
-// 8 x 2048 x 5120 bf16 forward: 122 us, 5.5 TB/s (84% of the measured copy bandwidth), issue slots
-// 62% busy; 8 x 2048 x 1536: forward 45 us, backward 88 us (4.0 TB/s); 131072 x 1536: 550 us, there the
+// 8 x 2048 x 5120 bf16 forward: 124 us, 5.4 TB/s (83% of the measured copy bandwidth), issue slots
+// 62% busy; 8 x 2048 x 1536: forward and backward 137 us, a third and two thirds; 131072 x 1536: 573 us, there the
 // tiles of a column that run at the same time wait for each other's maps.
 //
 // Per element the forward moves 4 I/O elements against 4 special-function operations (5 where a
@@ -781,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     if (kTma && w == kWarps + 1 && lane == 0) tma_store_wait_all();
 }
 
-// One token: V channels per thread, the rate worked out on the way.  64 x 5120 bf16: 4.6 us for 5 MB, a
-// launch's own latency.
+// One token: V channels per thread, the rate worked out on the way.  64 x 5120 bf16: 3.5 us for 5 MB as a
+// graph's node, a launch's own latency.
 template <typename T, int V>
 __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
     const int64_t cols = g.D / V;

@@ -10,7 +10,7 @@
 // fp32 quantity into the state (u or B scaled by f) goes in as three bf16 parts, the state
 // read by the outputs as two, and the entries of M are rounded to bf16 once, an error of the
 // same size as the rounding of the result.
-// 8 x 2048, 80 heads of 64 channels, 16 states, bf16 with gate: 242 us (508 MB, 2.1 TB/s); issue
+// 8 x 2048, 80 heads of 64 channels, 16 states, bf16 with gate: 244 us (508 MB, 2.1 TB/s); issue
 // slots 54% busy with three blocks per SM, no pipe above 30%: a chunk's steps wait for one another.
 #include <cuda_runtime.h>
 
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
     }
 }
 
-// 8 x 24 pairs, 32 chunks, 64 x 64 states: 31 us for 201 MB read and written once each.
+// 8 x 24 pairs, 32 chunks, 64 x 64 states: 30 us for 201 MB, each state read and written once.
 // Turns segment end states from zero into entering states, in place, for every (batch, head,
 // state): forward from `first` (h0 or zero) in segment order, or for the adjoint from zero in
 // reverse order.  The value after the last segment goes to `last`.
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
 // share the N states of a channel, four neighbouring ones each (V = 4, one 16-byte access) or one
 // at a time; a warp takes kStepRows channels per lane group of one (batch, head), so that the
 // scalars of that pair, some 80 instructions, are worked out once for 4 kStepRows states.  64 sequences,
-// 80 heads of 64 channels, 16 states: 14 us for 44 MB (3.1 TB/s; 120 us with a warp per channel).
+// 80 heads of 64 channels, 16 states: 11 us for 44 MB (4.0 TB/s, in part from L2).
 constexpr int kStepRows = 4;
 
 template <typename T, int LPR, int V>

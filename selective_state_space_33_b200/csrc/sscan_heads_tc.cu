@@ -4,9 +4,9 @@
 // With 128 states the chunk's products are 2 x 128 x (128 + 3 x 64 + 64 + 64) x 128 operations against 48 KB
 // of traffic; as mma.sync they kept eight warps loading fragments (1470 us at 65536 steps, 24 heads, 128
 // states, issue slots 45% busy, tensor pipe under 40%).  Here one thread issues them from
-// shared memory and tensor memory, and the warps only do what is elementwise: 640 us, of which the
-// output pass 460 and the pass over the segments' states 175.  What is left is the order of a chunk's
-// steps with one block per SM (issue slots 32%, tensor pipe 17% busy); barriers that keep the
+// shared memory and tensor memory, and the warps only do what is elementwise: 640 us, about
+// 72% of it the output pass and 27% the pass over the segments' states.  What is left is the order of a chunk's
+// steps with one block per SM (output pass: issue slots 37%, tensor pipe 18% busy); barriers that keep the
 // working warps in step are faster than mbarriers that let them drift (815 against 764 us at
 // that stage: drifting warps miss the instruction cache).
 //
@@ -164,7 +164,8 @@ __device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
 
 // The outputs of a thread's 16 channels at step t of a chunk with values of u that are not finite: such
 // values were left out of Yb, and the terms M_ts u_s that hold one are added for s <= t alone, from
-// global memory.  A function of its own: inlined, its registers cost the usual path a tenth of its time.
+// global memory.  A function of its own: inlined it costs the usual path about 1% (8 x 2048, 24 heads, 64
+// states, forward and backward: 885 against 875 us; 65536 steps, 128 states: 641 against 639).
 __device__ __noinline__ void rare_outputs(const HeadsArgs& a, const ChunkScalarsOf<kTcQ>& s, uint32_t ya_at, uint32_t yb_at,
                                           unsigned char* zb, int b, int h, int64_t t0, int t, int p0) {
     const bf16 *u = static_cast<const bf16*>(a.u), *B = static_cast<const bf16*>(a.B), *C = static_cast<const bf16*>(a.C);

@@ -13,7 +13,7 @@ constexpr int kSumGroups = 32;
 
 // put(c, sum over r of src[r * cols + c]): 32 columns by kSumGroups row groups per block;
 // group g adds rows g, g + kSumGroups, ... in order, then the groups are added in order.  256 rows of
-// 4608 columns: 5 us.
+// 4608 columns: 5.0-5.5 us.
 template <typename Put>
 __global__ void __launch_bounds__(32 * kSumGroups) rowsum_kernel(const float* __restrict__ src, int64_t rows,
                                                                 int64_t cols, Put put) {
