@@ -621,8 +621,9 @@ int64_t heads_slots(const HeadsArgs& a, bool bf16) {
 
 // Segments of a forward pass.  With fewer (batch, head) pairs than SMs a sequence is split into as
 // many segments, of at least four chunks, as fill the GPU once: a block more than it holds would
-// wait for a whole segment (65536 steps, 24 heads, 128 states: 25 segments, 600 blocks where 296
-// fit, 1750 us; 12 segments, 288 blocks, 1470 us).
+// wait for a whole segment (65536 steps, 24 heads: with 32 states, where 444 blocks fit, 18 segments,
+// 432 blocks, 535 us, 27 segments 673 us; with 128 states on tcgen05, where 148 fit, 6 segments 640 us,
+// 9 segments 840 us).
 void plan_segments(HeadsArgs& a, int64_t slots, int64_t least) {
     const int64_t bh = a.batch * a.H;
     int64_t nseg = 1;

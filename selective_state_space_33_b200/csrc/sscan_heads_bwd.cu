@@ -19,8 +19,8 @@
 // takes its inexact factor as three bf16 parts, 24 bits; M1 and the factors of the products
 // that end in bf16 are rounded once.
 // 8 x 2048, 24 heads of 64 channels, 64 states, bf16 with gate: 477 us; two blocks of eight warps per SM,
-// issue slots about a third busy, the rest the latency of nine products that follow one another (sixteen
-// warps of 64 registers were slower: 983 against 913 us for the whole forward and backward at that stage).
+// issue slots about a third busy, the rest the latency of nine products that follow one another
+// (sixteen warps of 64 registers were tried and were slower).
 #include <cuda_runtime.h>
 
 #include "sscan_heads.cuh"
