@@ -114,8 +114,10 @@ __device__ __forceinline__ float2 rsqrt2(float2 om) {
 }
 
 // a = exp(-s) and om = 1 - a^2 = e (2 - e), with e = 1 - a.  For s < 1/4, e comes from its Taylor
-// series to s^6 (the dropped s^7/5040 is below 1.3e-8 relative): the difference 1 - a would
-// cancel, and a long memory multiplies a's error by its length.  kAny: s may be 1/4 or more.
+// series to s^6 (the dropped s^7/5040 is below 5.5e-8 of e, the same size as e's rounding): the difference
+// 1 - a would cancel, and a long memory multiplies a's error by its length.  From 1/4 on (kAny: some s may
+// be there) a is the exponential itself, which keeps its relative precision however small it is (1 - e
+// would round it to a multiple of 2^-24, and every gradient through the state is a multiple of a).
 template <bool kAny>
 __device__ __forceinline__ void decay2(float2 s, float2& a, float2& om) {
     float2 p = fma2(s, splat(-1.f / 720.f), splat(1.f / 120.f));
@@ -124,11 +126,11 @@ __device__ __forceinline__ void decay2(float2 s, float2& a, float2& om) {
     p = fma2(s, p, splat(-0.5f));
     p = fma2(s, p, splat(1.f));
     float2 e = mul2(s, p);
-    if (kAny) {
-        if (!(s.x < 0.25f)) e.x = 1.f - ex2(-s.x * kLog2e);
-        if (!(s.y < 0.25f)) e.y = 1.f - ex2(-s.y * kLog2e);
-    }
     a = fma2(e, splat(-1.f), splat(1.f));
+    if (kAny) {
+        if (!(s.x < 0.25f)) a.x = ex2(-s.x * kLog2e), e.x = 1.f - a.x;
+        if (!(s.y < 0.25f)) a.y = ex2(-s.y * kLog2e), e.y = 1.f - a.y;
+    }
     om = mul2(e, fma2(e, splat(-1.f), splat(2.f)));
 }
 
