@@ -74,3 +74,87 @@ def test_strong_decay_of_a_state(cuda_device, io):
     sb.sscan_gated_step(x["u"][:, 0].contiguous(), x["a_raw"][:, 0].contiguous(), x["i_raw"][:, 0].contiguous(), x["Lam"],
                         state)
     assert (relative(state, a) <= limit(s[:, 0])).all()
+
+
+# m = sqrt(2 s) with s = c r: half of s's 20 * 2^-24 and a root, a product with i (10 * 2^-24) and with u: below
+# 64 * 2^-24 of a term.  L terms of one sign add up; each step rounds a (half of 2^-24 for a in [1/2, 1]) and the sum
+# (as much): at most L * 2^-24 of the result.
+def closed_limit(L, dtype=torch.float32):
+    return (L + 64) * EPS + (R.HALF_STEP[dtype] if dtype != torch.float32 else 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 70, 33])
+@pytest.mark.parametrize("gate,value", [("a_raw", -45.0), ("a_raw", -70.0), ("i_raw", -43.0), ("i_raw", -60.0)])
+def test_a_nearly_closed_gate_lets_through_what_it_should(cuda_device, io, D, gate, value):
+    """A decay gate at exp(-45) keeps a state and adds next to nothing to it, an input gate at exp(-60) adds
+    next to nothing to any: over 2000 steps both stay at what the definition gives, not at a
+    floor of the sigmoid."""
+    L = 2000
+    x = R.inputs("gated", 5, io, cuda_device, biases=False, batch=2, length=L, dim=D)
+    x["h0"].zero_()
+    x["u"] = x["u"].abs() + 0.5
+    x["i_raw"].fill_(0.5)
+    x["a_raw"].fill_(0.5)
+    x[gate].fill_(value)
+    out, last = sb.sscan_gated_fwd(**x, return_last_state=True)
+    ref, ref_last = R.gated(**{k: R.d64(v) for k, v in x.items()})
+    assert (relative(last, ref_last) <= closed_limit(L)).all()
+    assert (relative(out, ref) <= closed_limit(L, out.dtype)).all()
+    dout = torch.rand_like(x["u"]) + 0.5
+    g = sb.sscan_gated_bwd(x["u"], x["a_raw"], x["i_raw"], x["Lam"], dout, h0=x["h0"])
+    want = R.grads("gated", x, dout)
+    # no sum of these cancels: every term is of one sign
+    for k in ("du", "di_raw"):
+        assert (relative(g[k], want[k[1:]]) <= 2 * closed_limit(L, dout.dtype)).all(), k
+    state = x["h0"].clone()
+    for t in range(3):
+        p = R.token(x, t)
+        sb.sscan_gated_step(p["u"], p["a_raw"], p["i_raw"], x["Lam"], state)
+    assert (relative(state, R.d64(ref[:, 2])) <= closed_limit(3)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 33])
+def test_a_closed_gate_is_closed(cuda_device, io, D):
+    """-inf: nothing enters, exactly; a decay gate of -inf keeps the state, exactly, and takes no gradient."""
+    x = R.inputs("gated", 6, io, cuda_device, batch=2, length=300, dim=D)
+    y = {**x, "i_raw": torch.full_like(x["i_raw"], -float("inf")), "h0": torch.zeros_like(x["h0"])}
+    assert (sb.sscan_gated_fwd(**y) == 0).all()
+    y = {**x, "a_raw": torch.full_like(x["a_raw"], -float("inf"))}
+    out, last = sb.sscan_gated_fwd(**y, return_last_state=True)
+    assert torch.equal(last, x["h0"])
+    assert torch.equal(out, x["h0"].to(out.dtype)[:, None].expand_as(out))
+    dout = torch.ones_like(x["u"])
+    g = sb.sscan_gated_bwd(y["u"], y["a_raw"], y["i_raw"], y["Lam"], dout, y["a_bias"], y["i_bias"], y["h0"])
+    assert all((g[k] == 0).all() for k in ("du", "da_raw", "di_raw", "da_bias", "di_bias", "dLam"))
+    assert (g["dh0"] == 300).all()
+    state, p = x["h0"].clone(), R.token(y, 0)
+    sb.sscan_gated_step(p["u"], p["a_raw"], p["i_raw"], x["Lam"], state, x["a_bias"], x["i_bias"])
+    assert torch.equal(state, x["h0"])
+    # one masked stretch among ordinary tokens
+    z = {k: v.clone() for k, v in x.items()}
+    z["a_raw"][:, 100:200] = -float("inf")
+    out = sb.sscan_gated_fwd(**z)
+    # the state after each warp's 16 steps is put together from maps (a few fused products, exact but for
+    # their roundings: 16 * 2^-24 at most over the warps of a tile), then rounded
+    assert R.off(out[:, 100:200], out[:, 99:100].expand(-1, 100, -1)) <= 16 * EPS + (2 * R.HALF_STEP[out.dtype] if io == "bf16" else 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 33])
+@pytest.mark.parametrize("name,value", [("a_raw", float("nan")), ("a_raw", -float("inf")), ("i_raw", float("nan")),
+                                        ("i_raw", -100.0)])
+def test_one_extreme_gate_changes_nothing_else(cuda_device, io, D, name, value):
+    """Bit for bit: not the channel beside it, not the steps before it, not another batch row."""
+    x = R.inputs("gated", 8, io, cuda_device, batch=2, length=300, dim=D)
+    clean = sb.sscan_gated_fwd(**x)
+    x[name][1, 150, 3] = value
+    out = sb.sscan_gated_fwd(**x)
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[1, 150:, 3] = False
+    assert torch.equal(out[same], clean[same])
+    assert bool(torch.isnan(out[1, 150:, 3]).all()) == (value != value) and not torch.isnan(out[same]).any()
