@@ -376,8 +376,9 @@ typedef struct sscan_heads_problem {
 /* Bytes of workspace for op SSCAN_OP_FWD or SSCAN_OP_BWD (0 when none). */
 SSCAN_API size_t sscan_heads_workspace_size(const sscan_heads_problem* problem, int op);
 
-/* Steps are taken 64 at a time; a value that is not finite reaches only its own and later
- * steps, as in the recurrence. */
+/* Steps are taken 64 at a time, with bf16 and more than 32 states 128; a value that is not finite
+ * reaches only its own and later steps, as in the recurrence.  A state is infinite where the recurrence's
+ * is (exp(delta A) counts as above zero there); an out that depends on it may be NaN instead. */
 SSCAN_API sscan_status sscan_heads_fwd(const sscan_heads_problem* problem, const void* u, const void* delta_raw,
                                        const float* delta_bias, const float* A, const void* B, const void* C,
                                        const float* D_skip, const void* z, const float* h0, void* out,

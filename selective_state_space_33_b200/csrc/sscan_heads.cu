@@ -151,7 +151,7 @@ __device__ __forceinline__ void chunk_outputs(float (&y)[PTL][4], const T* C, co
 }
 
 template <typename T, int NT, int MODE>
-__global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>::blocks) heads_walk_kernel(HeadsArgs a, const T* dout) {
+__global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>::blocks) heads_walk_kernel(const __grid_constant__ HeadsArgs a, const T* dout) {
     using W = Walk<T, NT, MODE>;
     using M = Mma<T>;
     constexpr int PP = W::PITCH_P, PN = W::PITCH_N, WC = W::WC, kWork = 32 * W::NW;
@@ -213,12 +213,16 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
                 if (p < a.P && m < a.N) fn(S[j][i], (int64_t)p * a.N + m);
             }
     };
+    const bool handed = MODE == kWalkOut && a.ticket && seg > 0;
+    auto entering = [&]() -> const float* {  // null: zero
+        return MODE != kWalkOut          ? nullptr
+               : handed                  ? a.states + (bh * a.nseg + seg - 1) * a.P * a.N
+               : a.nseg > 1 && !a.ticket ? a.states + (bh * a.nseg + seg) * a.P * a.N
+               : a.h0                    ? a.h0 + bh * a.P * a.N
+                                         : nullptr;
+    };
     if (MODE == kWalkOut) {
-        const bool handed = a.ticket && seg > 0;
-        const float* first = handed                   ? a.states + (bh * a.nseg + seg - 1) * a.P * a.N
-                             : a.nseg > 1 && !a.ticket ? a.states + (bh * a.nseg + seg) * a.P * a.N
-                             : a.h0                    ? a.h0 + bh * a.P * a.N
-                                                       : nullptr;
+        const float* first = entering();
         if (W::stages == 2) {
             fetch(0);
             cp_async_commit();
@@ -428,6 +432,20 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
 #pragma unroll
             for (int k = 0; k < 4; ++k) S[j][k] = fmaf(dec, S[j][k], acc[j][k]);
     }
+    // an infinity or a NaN stays in the state once it is there
+    bool lost = false;
+#pragma unroll
+    for (int j = 0; j < NTL; ++j) lost = lost || not_finite(S[j]);
+    if (!kRev && lost) {
+        float v[4 * NTL];
+#pragma unroll
+        for (int j = 0; j < 4 * NTL; ++j) v[j] = S[j / 4][j % 4];
+        auto place = [p = p0 + g, m = n0 + 2 * q](int j) { return make_int2(p + (j >> 1 & 1) * 8, m + 8 * (j >> 2) + (j & 1)); };
+        const int64_t end = c1 * kQ;
+        state_by_steps<T, 4 * NTL>(v, place, a, b, h, c0 * kQ, end < a.L ? end : a.L, entering());
+#pragma unroll
+        for (int j = 0; j < 4 * NTL; ++j) S[j / 4][j % 4] = v[j];
+    }
     if (MODE == kWalkOut) {
         if (a.h_last && seg == a.nseg - 1) {
             float* o = a.h_last + bh * a.P * a.N;
@@ -483,7 +501,8 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
                 store_vec<V>(st + s * PN, cur);
                 const float e = ex2(d[k] * kLog2e);
 #pragma unroll
-                for (int v = 0; v < V; ++v) cur[v] = fmaf(e, cur[v], x[v]);
+                for (int v = 0; v < V; ++v)  // (an infinity is not decayed: e may have underflowed)
+                    cur[v] = fmaf(fabsf(cur[v]) > 3.4e38f ? 1.f : e, cur[v], x[v]);
             }
     }
     if (last) {

@@ -200,6 +200,50 @@ template <typename T, int NT> struct HeadsPitch {
     static constexpr int Q = kQ + Mma<T>::PAD;
 };
 
+// A thread's elements S[j], j < COUNT <= 64, of the state after steps t0 .. t1 - 1 of (b, h), at (p, n) = place(j):
+// those that are not finite are taken again from the state `first` before t0 (null: zero), step by
+// step.  A chunk's products split their operands in parts, and an infinity in one of them is not a number
+// there, where the recurrence has an infinity.  An infinity is not decayed here, since exp(q) may underflow.
+template <typename T, int COUNT, typename Place>
+__device__ __noinline__ void state_by_steps(float* S, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
+                                            int64_t t1, const float* first) {
+    const int grp = h / (a.H / a.G);
+    const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
+    unsigned long long todo = 0;
+#pragma unroll 1
+    for (int j = 0; j < COUNT; ++j) {
+        const int2 at = place(j);
+        if (fabsf(S[j]) <= 3.4e38f || at.x >= a.P || at.y >= a.N) continue;
+        todo |= 1ull << j;
+        S[j] = first ? first[(int64_t)at.x * a.N + at.y] : 0.f;
+    }
+#pragma unroll 1
+    for (int64_t t = t0; t < t1 && todo; ++t) {
+        const int64_t tok = b * a.L + t;
+        const float r = IO<T>::load(static_cast<const T*>(a.delta_raw), tok * a.H + h) + bias;
+        const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
+        const float q = dl * A, e = ex2(q * kLog2e), w = A != 0.f ? expm1f(q) / A : dl;
+#pragma unroll 1
+        for (unsigned long long left = todo; left; left &= left - 1) {
+            const int j = __ffsll((long long)left) - 1;
+            const int2 at = place(j);
+            const float x = w * IO<T>::load(static_cast<const T*>(a.u), (tok * a.H + h) * a.P + at.x) *
+                            IO<T>::load(static_cast<const T*>(a.B), (tok * a.G + grp) * a.N + at.y);
+            S[j] = fmaf(fabsf(S[j]) > 3.4e38f ? 1.f : e, S[j], x);
+            if (S[j] != S[j]) todo &= ~(1ull << j);  // and it stays so
+        }
+    }
+}
+
+// Whether any of a thread's elements is not finite.
+template <int COUNT>
+__device__ __forceinline__ bool not_finite(const float (&v)[COUNT]) {
+    float probe = 0.f;
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) probe = fmaf(v[j], 0.f, probe);
+    return probe != 0.f;
+}
+
 // Segment end states from zero (forward: of S; reverse: of its adjoint), and the carry
 // through them; sscan_heads.cu.
 void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, float* last, cudaStream_t st);

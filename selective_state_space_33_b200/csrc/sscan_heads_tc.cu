@@ -197,6 +197,25 @@ __device__ __noinline__ void rare_outputs(const HeadsArgs& a, const ChunkScalars
     }
 }
 
+// The state that enters a segment (null: zero).
+template <bool kOut>
+__device__ __forceinline__ const float* entering_state(const HeadsArgs& a, int64_t bh, int64_t seg) {
+    if (!kOut) return nullptr;
+    return a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N : a.h0 ? a.h0 + bh * a.P * a.N : nullptr;
+}
+
+// state_by_steps of a working thread's 16 elements over the block's segment; everything it needs is worked out
+// anew, which costs the usual path no registers.
+template <bool kOut>
+__device__ __noinline__ void segment_by_steps(float* S, const HeadsArgs& a) {
+    const int64_t seg = blockIdx.x / a.H, b = blockIdx.y;
+    const int h = (int)(blockIdx.x - seg * a.H), w = threadIdx.x >> 5;
+    const int row = 32 * (w & 3) + (threadIdx.x & 31), p0 = 16 * (w >> 2);
+    const int64_t t0 = seg * a.seg_chunks * kTcQ, end = t0 + a.seg_chunks * kTcQ;
+    state_by_steps<bf16, 16>(S, [p0, row](int k) { return make_int2(p0 + k, row); }, a, b, h, t0, end < a.L ? end : a.L,
+                             entering_state<kOut>(a, b * a.H + h, seg));
+}
+
 // kOut: outputs, from the state entering the segment; else the segment's end state from zero.
 template <int NT, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -337,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the state: row n = r, channels p0 .. p0 + 15
     float S[16];
     {
-        const float* first = !kOut ? nullptr : a.nseg > 1 ? a.states + (bh * a.nseg + seg) * a.P * a.N : a.h0 ? a.h0 + bh * a.P * a.N : nullptr;
+        const float* first = entering_state<kOut>(a, bh, seg);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const int p = p0 + k;
@@ -491,6 +510,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async();
         }
+    }
+    // an infinity or a NaN stays in the state once it is there
+    if (not_finite(S)) {
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = S[k];
+        segment_by_steps<kOut>(v, a);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[k] = v[k];
     }
     if (kOut) {
         if (a.h_last && seg == a.nseg - 1 && r < a.N) {
