@@ -205,7 +205,7 @@ template <typename T, int NT> struct HeadsPitch {
 // step.  A chunk's products split their operands in parts, and an infinity in one of them is not a number
 // there, where the recurrence has an infinity.  An infinity is not decayed here, since exp(q) may underflow.
 template <typename T, int COUNT, typename Place>
-__device__ __noinline__ void state_by_steps(float* S, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
+static __device__ __noinline__ void state_by_steps(float* S, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
                                             int64_t t1, const float* first) {
     const int grp = h / (a.H / a.G);
     const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
