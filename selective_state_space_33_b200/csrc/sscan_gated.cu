@@ -206,10 +206,18 @@ struct TileId {
 
 struct ChainSmem {
     TileId tile[4];          // by iteration
+    int gave_up;             // a wait for a copy ran out: this block starts no more
     float rate[2][64];       // rate softplus(Lam) of the tile's channels, by iteration
     float in[64];            // the state entering the tile
     float2 group[64];        // composed maps of the group's earlier tiles
 };
+
+// A copy has not come in time.  The block takes no tile after the one that it has drawn (a barrier's phase may be
+// incomplete), and tiles that wait for what it does not do give up in their turn.
+__device__ __forceinline__ void give_up(ChainSmem& s, unsigned int err) {
+    *reinterpret_cast<volatile int*>(&s.gave_up) = 1;
+    atomicOr(&g_device_error_gated, err);
+}
 
 // Barriers of a block besides 0: 1 the tile's maps are in shared memory (working warps and
 // carry_out's), 2 the entering state is (all warps), 3 the group's earlier tiles are composed
@@ -468,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     const CUtensorMap* const maps[3] = {&tm_a, &tm_i, &tm_u};
     if (threadIdx.x == 0) {
         sm.c.tile[0] = draw_tile(g, 0);
+        sm.c.gave_up = 0;
         if (kTma) {
             mbar_init(smem_u32(&sm.full[0]), 1);
             mbar_init(smem_u32(&sm.full[1]), 1);
@@ -486,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         const int buf = it & 1;
         if (w == kWarps + 1 && lane == 0) {
             // the last tile's outputs leave, then the next tile's inputs may take their place
-            const TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            const bool stop = kTma && *reinterpret_cast<volatile int*>(&sm.c.gave_up);
+            TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            if (stop) next.k = tiles;
             sm.c.tile[(it + 1) & 3] = next;
             const bool more = kTma && next.k < tiles;
             if (kTma && it > 0 && g.out) {
@@ -540,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         const int own = w * S * 32 * V + lv;
         T *ar = sm.rows[buf][0] + own, *ir = sm.rows[buf][1] + own, *u = sm.rows[buf][2] + own;
         if (kTma) {
-            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) atomicOr(&g_device_error_gated, 1u);
+            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) give_up(sm.c, 1u);
         } else {
             const int64_t r0 = (int64_t)t.k * ROWS, d0 = (int64_t)t.blk * 32 * V;
             fetch_rows<T, V, ROWS>(sm.rows[buf][0], g.a_raw, g, b, r0, d0);
@@ -602,7 +613,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         }
         if (kTma) fence_proxy_async();
     }
-    if (kTma && w == kWarps + 1 && lane == 0) tma_store_wait_all();
+    if (kTma && w == kWarps + 1 && lane == 0) {
+        tma_store_wait_all();
+        // every copy has been waited for, or is now: shared memory is given up with nothing in flight on it
+        if (*reinterpret_cast<volatile int*>(&sm.c.gave_up))
+            for (int k = 0; k < 2; ++k) mbar_drain(smem_u32(&sm.full[k]));
+    }
 }
 
 // The adjoint e_t that step t hands to h_{t-1} is affine in the one it gets: with
@@ -634,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     auto row_of = [&](const TileId& t) { return (int)(tiles - 1 - t.k) * ROWS; };
     if (threadIdx.x == 0) {
         sm.c.tile[0] = draw_tile(g, 0);
+        sm.c.gave_up = 0;
         if (kTma) {
             mbar_init(smem_u32(&sm.full[0]), 1);
             mbar_init(smem_u32(&sm.full[1]), 1);
@@ -651,7 +668,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         const TileId t = sm.c.tile[it & 3];
         const int buf = it & 1;
         if (w == kWarps + 1 && lane == 0) {
-            const TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            const bool stop = kTma && *reinterpret_cast<volatile int*>(&sm.c.gave_up);
+            TileId next = t.k < tiles ? draw_tile(g, it + 1) : t;
+            if (stop) next.k = tiles;
             sm.c.tile[(it + 1) & 3] = next;
             const bool more = kTma && next.k < tiles;
             if (kTma && it > 0) {
@@ -730,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             h[v] = live ? __ldg(g.ckpt_in + (b * g.chain.tiles + j) * g.D + d + v) : 0.f;
         }
         if (kTma) {
-            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) atomicOr(&g_device_error_gated, 2u);
+            if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) give_up(sm.c, 2u);
         } else {
             const int64_t r0 = j * ROWS, d0 = (int64_t)t.blk * 32 * V;
             fetch_rows<T, V, ROWS>(sm.rows[buf][0], g.dout, g, b, r0, d0);
@@ -834,7 +853,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             sm.red[2][w][lv + v] = siv[v];
         }
     }
-    if (kTma && w == kWarps + 1 && lane == 0) tma_store_wait_all();
+    if (kTma && w == kWarps + 1 && lane == 0) {
+        tma_store_wait_all();
+        // every copy has been waited for, or is now: shared memory is given up with nothing in flight on it
+        if (*reinterpret_cast<volatile int*>(&sm.c.gave_up))
+            for (int k = 0; k < 2; ++k) mbar_drain(smem_u32(&sm.full[k]));
+    }
 }
 
 // One token: V channels per thread, the rate worked out on the way.  64 x 5120 bf16: 3.5 us for 5 MB as a

@@ -50,7 +50,8 @@ struct TcSmem {
     alignas(1024) bf16 f[3][kTile];      // f U in three parts
     alignas(1024) bf16 S[kTile];         // [n][p]
     ChunkScalarsOf<kTcQ> s[4];           // by chunk
-    alignas(8) uint64_t full_x[2], full_b[2], full_c, full_z, scalars_ready[4], scalars_free[4], done_g, done_ya, done_st, done_yb;
+    alignas(8) uint64_t scalars_ready[4], scalars_free[4];
+    uint64_t full_x[2], full_b[2], full_c, full_z, done_g, done_ya, done_st, done_yb;  // copies and products
     uint32_t tmem;
 };
 
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool gate = kOut && a.z;
 
     if (tid == 0) {
-        for (uint64_t* bar = &sm.full_x[0]; bar <= &sm.done_yb; ++bar) mbar_init(smem_u32(bar), 1);
+        for (uint64_t* bar = &sm.scalars_ready[0]; bar <= &sm.done_yb; ++bar) mbar_init(smem_u32(bar), 1);
         fence_proxy_async();
     }
     if (w == 0) {
@@ -265,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (w == kIssuer) {
-        // one lane issues; the warp keeps the barriers
-        const bool one = lane == 0;
+        // one lane issues; the warp keeps the barriers.  Once its wait for a copy has given up it starts nothing more.
+        bool one = lane == 0;
         auto at = [&](int i) { return (int)((c0 + i) * kTcQ); };
         auto fetch = [&](bf16 (*dst)[kTile], int tiles, const CUtensorMap* map, int row, int i, uint64_t* bar) {
             mbar_expect_tx(smem_u32(bar), tiles * kTile * 2);
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
+            one = one && !late;
             if (kOut) work_or(0);
             else work_sync();
             if (one) {
@@ -344,6 +346,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_store_4d(&tm_out, 0, h, at(n - 1), b, smem_u32(sm.z));
                 tma_store_wait_all();
             }
+        }
+        // Shared and tensor memory are given up with nothing in flight on them: the last copies and products have
+        // been waited for, or are here, and after a wait that gave up each barrier once more.
+        if (lane == 0) {
+            wait(&sm.full_x[(n - 1) & 1], (n - 1) >> 1);
+            if (n > 1) wait(&sm.full_x[n & 1], (n - 2) >> 1);
+            wait(&sm.done_st, n - 1);
+            if (kOut) {
+                wait(&sm.full_z, n - 1);
+                wait(&sm.done_yb, n - 1);      // products end in order, so those before it have
+            }
+            if (late)
+                for (uint64_t* bar = &sm.full_x[0]; bar <= &sm.done_yb; ++bar) mbar_drain(smem_u32(bar));
         }
         __syncwarp();
         __syncthreads();

@@ -40,6 +40,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
     return false;
 }
 
+// After a wait has run out, before the block ends: whatever is still on its way to this mbarrier has come, or a
+// further limit has run out.  (One of the two phases is over at once.)
+__device__ __forceinline__ void mbar_drain(uint32_t bar) {
+    (void)mbar_wait(bar, 0, kWaitLimit / 64);
+    (void)mbar_wait(bar, 1, kWaitLimit / 64);
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                             uint32_t bar) {
     asm volatile(
