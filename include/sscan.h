@@ -420,7 +420,7 @@ SSCAN_API int sscan_debug_bounds(void);
  * receives the OR of every error bit raised since the last clear (bit 0: in a
  * forward kernel, bit 1: in the backward kernel, a bounded wait for an
  * asynchronous tile copy, or for an earlier tile's carry, gave up, so that the
- * kernel's outputs are incomplete or wrong; bit 2: sscan_probe_wait_timeout's wait ran out, as it is meant
+ * kernel's outputs are incomplete or wrong; bit 2: the wait of one of sscan_probe.h's timeout probes ran out, as it is meant
  * to; bit 3, debug build only: an index out of its array's range was caught and the
  * access skipped).  Returns SSCAN_ERR_TIMEOUT when any bit is set, SSCAN_OK when none is.
  * clear != 0 resets the word after reading.  Synchronous: it waits for work

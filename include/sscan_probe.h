@@ -36,6 +36,17 @@ SSCAN_API sscan_status sscan_probe_ex2(float* sink, int64_t iters, int blocks, i
  */
 SSCAN_API sscan_status sscan_probe_wait_timeout(unsigned int polls, void* stream);
 
+/*
+ * The same for the waits of the layers around the scan, each through the kernels' own code, on words, a flag
+ * or a barrier that nothing sets: the gated recurrence's wait for earlier tiles (three waits of `polls` polls),
+ * the multi-head forward's for the state an earlier segment hands on, and its tcgen05 form's for a copy or product
+ * (with the bounded drain that follows it).  Each sets bit 2 of the device status word.
+ */
+#define SSCAN_WAIT_CARRY 0
+#define SSCAN_WAIT_HANDED_STATE 1
+#define SSCAN_WAIT_PRODUCT 2
+SSCAN_API sscan_status sscan_probe_layer_wait_timeout(int wait, unsigned int polls, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -117,6 +117,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.sscan_device_status.restype = ctypes.c_int
     lib.sscan_probe_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.sscan_probe_wait_timeout.restype = ctypes.c_int
+    lib.sscan_probe_layer_wait_timeout.argtypes = [ctypes.c_int, ctypes.c_uint, vp]
+    lib.sscan_probe_layer_wait_timeout.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -717,3 +719,12 @@ def probe_wait_timeout(polls: int = 4096, *, stream=None):
     """Enqueue the bounded-wait self-test: one thread waits on a barrier nothing
     arrives on, gives up after ``polls`` polls and raises bit 2 of the device status."""
     _check(load_library().sscan_probe_wait_timeout(polls, _stream(stream)))
+
+
+LAYER_WAITS = {"carry": 0, "handed_state": 1, "product": 2}
+
+
+def probe_layer_wait_timeout(wait: str, polls: int = 4096, *, stream=None):
+    """The same for a wait of the layers' kernels: "carry" (gated recurrence), "handed_state" or
+    "product" (multi-head forward)."""
+    _check(load_library().sscan_probe_layer_wait_timeout(LAYER_WAITS[wait], polls, _stream(stream)))

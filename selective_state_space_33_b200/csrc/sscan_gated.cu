@@ -169,13 +169,13 @@ __device__ __forceinline__ void put_word(unsigned long long* p, float a, float h
 // words after the one before, onto (A, H); false when one did not come in time.
 template <int V>
 __device__ __forceinline__ bool take_maps(const unsigned long long* words, int64_t first, int64_t extent, int n,
-                                          float (&A)[V], float (&H)[V]) {
+                                          float (&A)[V], float (&H)[V], uint32_t limit) {
     // a map that is not asked for is the identity (1, 0)
     unsigned long long m[kFan - 1][V];
     const unsigned long long* p = words + first;
     bool ready = false;
 #pragma unroll 1
-    for (uint32_t tries = 0; tries < kPollLimit && !ready; ++tries) {
+    for (uint32_t tries = 0; tries < limit && !ready; ++tries) {
         ready = true;
 #pragma unroll
         for (int i = 0; i < kFan - 1; ++i)
@@ -234,26 +234,26 @@ __device__ __forceinline__ bool closes_super(unsigned int k) { return k % (kFan 
 // wait that gives up raises `err` and goes on with what it has, and so do the tiles after it.
 template <int V>
 __device__ __forceinline__ void carry_in(const Chain& c, const TileId& t, const float (&first)[V], float (&state)[V],
-                                         ChainSmem& s, unsigned int err) {
+                                         ChainSmem& s, unsigned int err, uint32_t limit = kPollLimit) {
     const int lane = threadIdx.x & 31;
     const int64_t k = t.k, g = k / kFan, sp = g / kFan, W = 32 * V;
     float A[V], H[V], Ag[V], Hg[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = Ag[v] = 1.f, H[v] = Hg[v] = 0.f, state[v] = first[v];
     const int64_t lv = lane * V;
-    bool ok = take_maps<V>(c.maps, (t.col * c.tiles + g * kFan) * W + lv, c.cols * c.tiles * W, (int)(k - g * kFan), A, H);
+    bool ok = take_maps<V>(c.maps, (t.col * c.tiles + g * kFan) * W + lv, c.cols * c.tiles * W, (int)(k - g * kFan), A, H, limit);
     if (closes_group(t.k)) {
 #pragma unroll
         for (int v = 0; v < V; ++v) s.group[lv + v] = make_float2(A[v], H[v]);
         sync_group();
     }
-    ok = take_maps<V>(c.groups, (t.col * c.ngroups + sp * kFan) * W + lv, c.cols * c.ngroups * W, (int)(g - sp * kFan), Ag, Hg) && ok;
+    ok = take_maps<V>(c.groups, (t.col * c.ngroups + sp * kFan) * W + lv, c.cols * c.ngroups * W, (int)(g - sp * kFan), Ag, Hg, limit) && ok;
     if (sp > 0) {
         const int64_t at = (t.col * c.nsupers + sp) * W + lv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             unsigned long long m = kUnset;
-            for (uint32_t tries = 0; tries < kPollLimit && m == kUnset; ++tries) {
+            for (uint32_t tries = 0; tries < limit && m == kUnset; ++tries) {
                 if (tries) __nanosleep(32);
                 m = in_range(at + v, c.cols * c.nsupers * W) ? poll_word(c.states + at + v) : 0ull;
             }
@@ -913,6 +913,24 @@ struct GatedGradPut {
     }
 };
 
+// carry_in made to run out of polls, for a tile that waits for a map, a group and a state which nothing sets.
+constexpr int kProbeTile = kFan * kFan + kFan + 1;
+__device__ unsigned long long g_probe_words[32 * (kProbeTile + 1)];
+
+__global__ void __launch_bounds__(32) carry_probe_kernel(unsigned int polls) {
+    __shared__ ChainSmem s;
+    for (int i = threadIdx.x; i < 32 * (kProbeTile + 1); i += 32) g_probe_words[i] = kUnset;
+    __threadfence();
+    __syncwarp();
+    Chain c{};
+    c.maps = c.groups = c.states = g_probe_words;
+    c.tiles = c.ngroups = c.nsupers = kProbeTile + 1;
+    c.cols = 1;
+    const float first[1] = {0.f};
+    float state[1];
+    carry_in<1>(c, TileId{kProbeTile, 0, 0, 0}, first, state, s, 4u, polls);
+}
+
 // ---------------------------------------------------------------- host
 
 sscan_status check_gated(const sscan_gated_problem* p) {
@@ -1075,6 +1093,11 @@ void step_blocks(const GatedArgs& g, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_carry_probe(unsigned int polls, cudaStream_t st) {
+    carry_probe_kernel<<<1, 32, 0, st>>>(polls);
+    return cudaGetLastError();
+}
 
 cudaError_t read_device_error_gated(unsigned int* value, int clear) {
     cudaError_t e = cudaMemcpyFromSymbol(value, g_device_error_gated, sizeof(unsigned int));

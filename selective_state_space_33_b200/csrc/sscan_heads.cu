@@ -64,8 +64,8 @@ struct Walk {
 };
 
 // A state handed from one segment's block to the next.
-__device__ __forceinline__ bool wait_handed(const unsigned int* p) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+__device__ __forceinline__ bool wait_handed(const unsigned int* p, uint32_t limit = kWaitLimit) {
+    for (uint32_t i = 0; i < limit; ++i) {
         unsigned int v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
         if (v) return true;
@@ -582,6 +582,12 @@ __global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* sta
     }
 }
 
+// wait_handed made to run out of polls, on a flag that nothing sets.
+__device__ unsigned int g_probe_flag = 0;
+__global__ void handed_probe_kernel(unsigned int polls) {
+    if (!wait_handed(&g_probe_flag, polls)) atomicOr(&g_device_error_walk, 4u);
+}
+
 // ---------------------------------------------------------------- host
 
 template <typename T, int NT, int MODE>
@@ -736,6 +742,11 @@ void launch_heads_carry(const HeadsArgs& a, bool reverse, const float* first, fl
     if (four) heads_carry_kernel<4><<<blocks, 128, 0, st>>>(a, reverse, first, last);
     else heads_carry_kernel<1><<<blocks, 128, 0, st>>>(a, reverse, first, last);
     api_count_launch();
+}
+
+cudaError_t launch_handed_probe(unsigned int polls, cudaStream_t st) {
+    handed_probe_kernel<<<1, 1, 0, st>>>(polls);
+    return cudaGetLastError();
 }
 
 cudaError_t read_device_error_walk(unsigned int* value, int clear) {

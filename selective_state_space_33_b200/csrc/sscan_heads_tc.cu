@@ -554,6 +554,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols));
 }
 
+// A wait made to run out of polls, on a barrier that nothing arrives on, and the barrier drained after it.
+__global__ void product_probe_kernel(unsigned int polls) {
+    __shared__ __align__(8) uint64_t bar;
+    mbar_init(smem_u32(&bar), 1);
+    fence_proxy_async();
+    if (mbar_wait(smem_u32(&bar), 0, polls)) return;
+    mbar_drain(smem_u32(&bar));
+    atomicOr(&g_device_error_heads, 4u);
+}
+
 // A map over (batch, L, heads or groups, width) with boxes of 128 steps by 64 of the width, zeros outside.
 bool tc_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t L, int64_t batch) {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -595,6 +605,11 @@ cudaError_t launch(const HeadsArgs& a, cudaStream_t st) {
 cudaError_t launch_heads_tc(const HeadsArgs& a, bool local, cudaStream_t st) {
     if (a.N <= 64) return local ? launch<64, false>(a, st) : launch<64, true>(a, st);
     return local ? launch<128, false>(a, st) : launch<128, true>(a, st);
+}
+
+cudaError_t launch_product_probe(unsigned int polls, cudaStream_t st) {
+    product_probe_kernel<<<1, 1, 0, st>>>(polls);
+    return cudaGetLastError();
 }
 
 cudaError_t read_device_error_heads(unsigned int* value, int clear) {

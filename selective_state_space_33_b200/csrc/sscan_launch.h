@@ -178,6 +178,13 @@ cudaError_t read_device_error_gated(unsigned int* value, int clear);
 cudaError_t read_device_error_heads(unsigned int* value, int clear);
 cudaError_t read_device_error_walk(unsigned int* value, int clear);
 
+// The waits of the layers' kernels, made to run out after `polls` polls: the gated recurrence's for its carry, the
+// multi-head forward's for a handed-on state, and its tcgen05 form's for a copy or product.  Each raises bit 2
+// of its own error word.
+cudaError_t launch_carry_probe(unsigned int polls, cudaStream_t st);
+cudaError_t launch_handed_probe(unsigned int polls, cudaStream_t st);
+cudaError_t launch_product_probe(unsigned int polls, cudaStream_t st);
+
 // One thread waits, with the kernels' bounded wait cut to `polls` polls, on an
 // mbarrier that nothing arrives on, then raises bit 2 of the device error word.
 cudaError_t launch_wait_probe(unsigned int polls, cudaStream_t st);

@@ -36,3 +36,14 @@ extern "C" sscan_status sscan_probe_wait_timeout(unsigned int polls, void* strea
     return sscan::launch_wait_probe(polls, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSCAN_OK
                                                                                             : SSCAN_ERR_CUDA;
 }
+
+extern "C" sscan_status sscan_probe_layer_wait_timeout(int wait, unsigned int polls, void* stream) {
+    if (polls == 0 || polls > (1u << 20)) return SSCAN_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (wait == SSCAN_WAIT_CARRY) e = sscan::launch_carry_probe(polls, st);
+    else if (wait == SSCAN_WAIT_HANDED_STATE) e = sscan::launch_handed_probe(polls, st);
+    else if (wait == SSCAN_WAIT_PRODUCT) e = sscan::launch_product_probe(polls, st);
+    else return SSCAN_ERR_INVALID_ARG;
+    return e == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
+}
