@@ -47,6 +47,15 @@ SSCAN_API sscan_status sscan_probe_wait_timeout(unsigned int polls, void* stream
 #define SSCAN_WAIT_PRODUCT 2
 SSCAN_API sscan_status sscan_probe_layer_wait_timeout(int wait, unsigned int polls, void* stream);
 
+
+/*
+ * A test of the debug build's index checks (sscan_debug_bounds): from now on they take every array to be `elements`
+ * (0 .. 2^20) shorter than it is, so that accesses to its last elements are reported as bad and skipped.  No access
+ * leaves its array; results are incomplete until the number is 0 again.  Synchronous, for the current
+ * device.  The release build returns SSCAN_ERR_UNSUPPORTED.
+ */
+SSCAN_API sscan_status sscan_debug_shorten(int64_t elements);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,16 +18,21 @@ constexpr unsigned int kErrBounds = 8u;
 
 #ifdef SSCAN_DEBUG_BOUNDS
 extern __device__ unsigned int g_device_error;
+// Elements by which every array counts as shorter than it is, 0 but in a test of the checks themselves
+// (sscan_debug_shorten): the arrays' last elements are then reported and skipped.
+extern __device__ long long g_debug_shorten;
 #endif
 
-__device__ __forceinline__ bool in_range(int64_t i, int64_t n) {
+// Whether the `count` elements from i on lie in an array of n.
+__device__ __forceinline__ bool in_range(int64_t i, int64_t n, int count = 1) {
 #ifdef SSCAN_DEBUG_BOUNDS
-    if (i >= 0 && i < n) return true;
+    if (i >= 0 && i + count <= n - g_debug_shorten) return true;
     atomicOr(&g_device_error, kErrBounds);
     return false;
 #else
     (void)i;
     (void)n;
+    (void)count;
     return true;
 #endif
 }

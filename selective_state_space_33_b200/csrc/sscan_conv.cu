@@ -12,6 +12,7 @@
 
 #include <initializer_list>
 
+#include "sscan_check.cuh"
 #include "sscan_host.h"
 #include "sscan_math.cuh"
 #include "sscan_rowsum.cuh"
@@ -45,7 +46,7 @@ template <typename T, int K, int V>
 __device__ __forceinline__ void load_row(const ConvArgs& a, int64_t b, int64_t t, int64_t d, float (&x)[V]) {
     if (t >= 0) {
         load_vec<V>(static_cast<const T*>(a.u) + (b * a.L + t) * a.D + d, x);
-    } else if (a.state0) {
+    } else if (a.state0 && in_range((b * (K - 1) + t + K - 1) * a.D + d, a.batch * (K - 1) * a.D, V)) {
         load_vec<V>(static_cast<const T*>(a.state0) + (b * (K - 1) + t + K - 1) * a.D + d, x);
     } else {
 #pragma unroll
@@ -59,14 +60,18 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int64_t d, float (&
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const float* p = a.w + (d + v) * K;
-        if (K == 4 && a.wide_w) {
+        const bool in = in_range((d + v) * K, a.D * K, K);
+        if (!in) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][v] = 0.f;
+        } else if (K == 4 && a.wide_w) {
             const float4 f = __ldg(reinterpret_cast<const float4*>(p));
             w[0][v] = f.x, w[1][v] = f.y, w[K - 2][v] = f.z, w[K - 1][v] = f.w;
         } else {
 #pragma unroll
             for (int k = 0; k < K; ++k) w[k][v] = __ldg(p + k);
         }
-        bias[v] = a.bias ? __ldg(a.bias + d + v) : 0.f;
+        bias[v] = a.bias && in_range(d + v, a.D) ? __ldg(a.bias + d + v) : 0.f;
     }
 }
 
@@ -130,7 +135,8 @@ __global__ void __launch_bounds__(128, 8) conv_fwd_kernel(ConvArgs a) {
         // the window now holds the last K - 1 inputs; each was read exactly, so this is a copy
 #pragma unroll
         for (int k = 0; k < K - 1; ++k)
-            store_vec<V>(static_cast<T*>(a.last) + (b * (K - 1) + k) * a.D + d, x[k]);
+            if (in_range((b * (K - 1) + k) * a.D + d, a.batch * (K - 1) * a.D, V))
+                store_vec<V>(static_cast<T*>(a.last) + (b * (K - 1) + k) * a.D + d, x[k]);
     }
 }
 
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a
             if (s >= K - 1) {
                 store_vec<V>(dp, dx);
                 dp += a.D;
-            } else if (t0 == 0 && a.dstate0) {
+            } else if (t0 == 0 && a.dstate0 && in_range((b * (K - 1) + s) * a.D + d, a.batch * (K - 1) * a.D, V)) {
                 store_vec<V>(static_cast<T*>(a.dstate0) + (b * (K - 1) + s) * a.D + d, dx);
             }
         };
@@ -253,7 +259,10 @@ __global__ void __launch_bounds__(32 * kBwdGroups, 3) conv_bwd_kernel(ConvArgs a
         }
         if (d < a.D) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.part[((int64_t)blockIdx.y * (K + 1) + k) * a.D + d + v] = s[v];
+            for (int v = 0; v < V; ++v) {
+                const int64_t at = ((int64_t)blockIdx.y * (K + 1) + k) * a.D + d + v;
+                if (in_range(at, a.batch * a.tiles * (K + 1) * a.D)) a.part[at] = s[v];
+            }
         }
     }
 }
@@ -268,9 +277,13 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
     if (b >= a.batch) return;
     const int64_t d = (i - b * cols) * V;
     T* sp = static_cast<T*>(a.last) + b * (K - 1) * a.D + d;
+    auto held = [&](int k) { return in_range((b * (K - 1) + k) * a.D + d, a.batch * (K - 1) * a.D, V); };
     Vec<T, V> in[K];
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) in[k].load_rw(sp + k * a.D);
+    for (int k = 0; k < K - 1; ++k) {
+        in[k].zero();
+        if (held(k)) in[k].load_rw(sp + k * a.D);
+    }
     in[K - 1].load(static_cast<const T*>(a.u) + b * a.D + d);
     float w[K][V], y[V];
     load_taps<K, V>(a, d, w, y);
@@ -287,7 +300,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
     }
     store_vec<V>(static_cast<T*>(a.out) + b * a.D + d, y);
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) in[k + 1].store(sp + k * a.D);
+    for (int k = 0; k < K - 1; ++k)
+        if (held(k)) in[k + 1].store(sp + k * a.D);
 }
 
 // Partial rows are [K + 1][D]: K columns of dweight (D, K), then dbias (D).
@@ -297,8 +311,11 @@ struct ConvGradPut {
     int64_t D, K;
     __device__ void operator()(int64_t c, float s) const {
         const int64_t k = c / D, d = c - k * D;
-        if (k < K) dweight[d * K + k] = s;
-        else if (dbias) dbias[d] = s;
+        if (k < K) {
+            if (in_range(d * K + k, D * K)) dweight[d * K + k] = s;
+        } else if (dbias && in_range(d, D)) {
+            dbias[d] = s;
+        }
     }
 };
 

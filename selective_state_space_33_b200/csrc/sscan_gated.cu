@@ -318,7 +318,7 @@ __device__ __forceinline__ void fill_rates(const GatedArgs& g, const TileId& t, 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t x = (int64_t)t.blk * 32 * V + v * 32 + lane;
-        rates[v * 32 + lane] = x < g.D ? decay_rate(__ldg(g.Lam + x), g.rate) : 0.f;
+        rates[v * 32 + lane] = x < g.D && in_range(x, g.D) ? decay_rate(__ldg(g.Lam + x), g.rate) : 0.f;
     }
 }
 
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         if (w == kWarps) {
             float first[V], state[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) first[v] = live && g.h0 ? __ldg(g.h0 + b * g.D + d + v) : 0.f;
+            for (int v = 0; v < V; ++v) first[v] = live && g.h0 && in_range(b * g.D + d + v, g.batch * g.D) ? __ldg(g.h0 + b * g.D + d + v) : 0.f;
             carry_in<V>(g.chain, t, first, state, sm.c, 1u);
             sync_state();
             continue;
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             publish_state<V>(g.chain, t, H);
             if (live && g.h_last && t.k == tiles - 1) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) g.h_last[b * g.D + d + v] = H[v];
+                for (int v = 0; v < V; ++v)
+                    if (in_range(b * g.D + d + v, g.batch * g.D)) g.h_last[b * g.D + d + v] = H[v];
             }
             continue;
         }
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && g.a_bias ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
-            nib[v] = live && g.i_bias ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
         }
         const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
         const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
@@ -601,7 +602,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         if (g.ckpt && t0 % kCkpt == 0 && t0 < g.L && live) {
             const int64_t rows = (g.L + kCkpt - 1) / kCkpt;
 #pragma unroll
-            for (int v = 0; v < V; ++v) g.ckpt[(b * rows + t0 / kCkpt) * g.D + d + v] = h[v];
+            for (int v = 0; v < V; ++v) {
+                const int64_t at = (b * rows + t0 / kCkpt) * g.D + d + v;
+                if (in_range(at, g.batch * rows * g.D)) g.ckpt[at] = h[v];
+            }
         }
         if (!g.out) continue;
 #pragma unroll
@@ -695,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
                     float s = 0.f;
 #pragma unroll
                     for (int q = 0; q < kWarps; ++q) s += sm.red[w][q][lv + v];
-                    g.part[(((int64_t)p.b * g.chain.tiles + j) * 3 + w) * g.D + d + v] = s;
+                    const int64_t at = (((int64_t)p.b * g.chain.tiles + j) * 3 + w) * g.D + d + v;
+                    if (in_range(at, g.batch * g.chain.tiles * 3 * g.D)) g.part[at] = s;
                 }
             }
         }
@@ -733,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             publish_state<V>(g.chain, t, E);
             if (live && g.dh0 && j == 0) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) g.dh0[b * g.D + d + v] = E[v];
+                for (int v = 0; v < V; ++v)
+                    if (in_range(b * g.D + d + v, g.batch * g.D)) g.dh0[b * g.D + d + v] = E[v];
             }
             continue;
         }
@@ -744,9 +750,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V], h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && g.a_bias ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
-            nib[v] = live && g.i_bias ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
-            h[v] = live ? __ldg(g.ckpt_in + (b * g.chain.tiles + j) * g.D + d + v) : 0.f;
+            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+            const int64_t at = (b * g.chain.tiles + j) * g.D + d + v;
+            h[v] = live && in_range(at, g.batch * g.chain.tiles * g.D) ? __ldg(g.ckpt_in + at) : 0.f;
         }
         if (kTma) {
             if (!mbar_wait(smem_u32(&sm.full[buf]), (it >> 1) & 1) && lane == 0) give_up(sm.c, 2u);
@@ -872,7 +879,9 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
     const int64_t d = (i - b * cols) * V, at = b * g.D + d;
     float u[V], ar[V], ir[V], h[V];
     Vec<float, V> hs;
-    hs.load_rw(g.state + at);
+    hs.zero();
+    const bool held = in_range(at, g.batch * g.D, V), params = in_range(d, g.D, V);
+    if (held) hs.load_rw(g.state + at);
     load_vec<V>(static_cast<const T*>(g.u) + at, u);
     load_vec<V>(static_cast<const T*>(g.a_raw) + at, ar);
     load_vec<V>(static_cast<const T*>(g.i_raw) + at, ir);
@@ -882,9 +891,10 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
         // V = 1 computes its one element twice
         const int v1 = V == 1 ? 0 : v + 1;
         float2 r, i, a, om, nab = splat(0.f), nib = splat(0.f);
-        if (g.a_bias) nab = make_float2(-kLog2e * __ldg(g.a_bias + d + v), -kLog2e * __ldg(g.a_bias + d + v1));
-        if (g.i_bias) nib = make_float2(-kLog2e * __ldg(g.i_bias + d + v), -kLog2e * __ldg(g.i_bias + d + v1));
-        const float2 c = make_float2(decay_rate(__ldg(g.Lam + d + v), g.rate), decay_rate(__ldg(g.Lam + d + v1), g.rate));
+        if (g.a_bias && params) nab = make_float2(-kLog2e * __ldg(g.a_bias + d + v), -kLog2e * __ldg(g.a_bias + d + v1));
+        if (g.i_bias && params) nib = make_float2(-kLog2e * __ldg(g.i_bias + d + v), -kLog2e * __ldg(g.i_bias + d + v1));
+        const float2 c = !params ? splat(0.f)
+                                 : make_float2(decay_rate(__ldg(g.Lam + d + v), g.rate), decay_rate(__ldg(g.Lam + d + v1), g.rate));
         const float2 xr = make_float2(ar[v], ar[v1]), xi = make_float2(ir[v], ir[v1]);
         r = gate2(xr, nab);
         i = gate2(xi, nib);
@@ -895,7 +905,7 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
         if (V > 1) h[v1] = hn.y;
     }
     hs.set(h);
-    hs.store(g.state + at);
+    if (held) hs.store(g.state + at);
     store_vec<V>(static_cast<T*>(g.out) + at, h);
 }
 
@@ -907,6 +917,7 @@ struct GatedGradPut {
     int64_t D;
     __device__ void operator()(int64_t c, float s) const {
         const int64_t k = c / D, d = c - k * D;
+        if (!in_range(d, D)) return;
         if (k == 0) dLam[d] = s * rate / (1.f + expf(-Lam[d]));
         else if (k == 1 && da_bias) da_bias[d] = s;
         else if (k == 2 && di_bias) di_bias[d] = s;

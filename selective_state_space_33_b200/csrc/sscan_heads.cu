@@ -228,10 +228,16 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             cp_async_commit();
         }
         if (handed) {
-            if (tid == 0 && !wait_handed(a.handed + bh * a.nseg + seg - 1)) raise_heads_error();
+            if (tid == 0 && in_range(bh * a.nseg + seg - 1, segments(a)) && !wait_handed(a.handed + bh * a.nseg + seg - 1)) raise_heads_error();
             product_sync<kWork>();
         }
-        if (first) each_state([&](float& v, int64_t at) { v = __ldcg(first + at); });
+        if (first) {
+            const int64_t base = handed ? bh * a.nseg + seg - 1 : a.nseg > 1 && !a.ticket ? bh * a.nseg + seg : bh;
+            const int64_t extent = a.nseg > 1 && (handed || !a.ticket) ? states_extent(a) : state_extent(a);
+            each_state([&](float& v, int64_t at) {
+                if (in_range(base * a.P * a.N + at, extent)) v = __ldcg(first + at);
+            });
+        }
     }
     double total = 0.0;
     if (MODE != kWalkOut && W::stages == 2) {
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
             else __syncwarp();
             T* stage = W::big ? t.C : sm.z;
             constexpr int PS = W::big ? PN : PP;
-            const float D = a.D ? __ldg(a.D + h) : 0.f;
+            const float D = head_param(a, a.D, h);
 #pragma unroll
             for (int j = 0; j < PTL; ++j)
 #pragma unroll
@@ -449,19 +455,25 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
     if (MODE == kWalkOut) {
         if (a.h_last && seg == a.nseg - 1) {
             float* o = a.h_last + bh * a.P * a.N;
-            each_state([&](float& v, int64_t at) { o[at] = v; });
+            each_state([&](float& v, int64_t at) {
+                if (in_range(bh * a.P * a.N + at, state_extent(a))) o[at] = v;
+            });
         }
         if (a.ticket && seg < a.nseg - 1) {
             float* o = a.states + (bh * a.nseg + seg) * a.P * a.N;
-            each_state([&](float& v, int64_t at) { __stcg(o + at, v); });
+            each_state([&](float& v, int64_t at) {
+                if (in_range((bh * a.nseg + seg) * a.P * a.N + at, states_extent(a))) __stcg(o + at, v);
+            });
             __threadfence();
             product_sync<kWork>();
-            if (tid == 0) hand_on(a.handed + bh * a.nseg + seg);
+            if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) hand_on(a.handed + bh * a.nseg + seg);
         }
     } else {
         float* o = a.states + (bh * a.nseg + seg) * a.P * a.N;
-        each_state([&](float& v, int64_t at) { o[at] = v; });
-        if (tid == 0) a.decays[bh * a.nseg + seg] = (float)total;
+        each_state([&](float& v, int64_t at) {
+            if (in_range((bh * a.nseg + seg) * a.P * a.N + at, states_extent(a))) o[at] = v;
+        });
+        if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) a.decays[bh * a.nseg + seg] = (float)total;
     }
 }
 
@@ -480,7 +492,8 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
     const float* dec = a.decays + bh * a.nseg;
     float cur[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) cur[v] = first ? first[bh * PN + at + v] : 0.f;
+    for (int v = 0; v < V; ++v) cur[v] = first && in_range(bh * PN + at + v, state_extent(a)) ? first[bh * PN + at + v] : 0.f;
+    auto held = [&](int64_t s) { return in_range((bh * a.nseg + s) * PN + at, states_extent(a), V); };
     constexpr int kAhead = 8;
     for (int64_t k0 = 0; k0 < a.nseg; k0 += kAhead) {
         Vec<float, V> loc[kAhead];
@@ -489,8 +502,9 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
         for (int k = 0; k < kAhead; ++k)
             if (k0 + k < a.nseg) {
                 const int64_t s = reverse ? a.nseg - 1 - (k0 + k) : k0 + k;
-                loc[k].load_rw(st + s * PN);
-                d[k] = dec[s];
+                loc[k].zero();
+                if (held(s)) loc[k].load_rw(st + s * PN);
+                d[k] = in_range(bh * a.nseg + s, segments(a)) ? dec[s] : 0.f;
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
@@ -498,7 +512,7 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
                 const int64_t s = reverse ? a.nseg - 1 - (k0 + k) : k0 + k;
                 float x[V];
                 loc[k].get(x);
-                store_vec<V>(st + s * PN, cur);
+                if (held(s)) store_vec<V>(st + s * PN, cur);
                 const float e = ex2(d[k] * kLog2e);
 #pragma unroll
                 for (int v = 0; v < V; ++v)  // (an infinity is not decayed: e may have underflowed)
@@ -507,7 +521,8 @@ __global__ void __launch_bounds__(128) heads_carry_kernel(HeadsArgs a, bool reve
     }
     if (last) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) last[bh * PN + at + v] = cur[v];
+        for (int v = 0; v < V; ++v)
+            if (in_range(bh * PN + at + v, state_extent(a))) last[bh * PN + at + v] = cur[v];
     }
 }
 
@@ -533,17 +548,19 @@ __global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* sta
 
     float x[kStepRows], zv[kStepRows];
     Vec<float, V> s[kStepRows];
+    auto held = [&](int p, int n) { return in_range((bh * a.P + p) * a.N + n, state_extent(a), V); };
     const bool one = V * LPR >= a.N;  // every state of a channel is in one access of its lanes
 #pragma unroll
     for (int k = 0; k < kStepRows; ++k) {
         const int p = p0 + k * RW;
         if (p >= a.P) continue;
-        if (one && l * V < a.N) s[k].load_rw(state + (bh * a.P + p) * a.N + l * V);
+        s[k].zero();
+        if (one && l * V < a.N && held(p, l * V)) s[k].load_rw(state + (bh * a.P + p) * a.N + l * V);
         x[k] = IO<T>::load(static_cast<const T*>(a.u), bh * a.P + p);
         zv[k] = a.z ? IO<T>::load(static_cast<const T*>(a.z), bh * a.P + p) : 0.f;
     }
-    const float A = __ldg(a.A + h), D = a.D ? __ldg(a.D + h) : 0.f;
-    const float r = IO<T>::load(static_cast<const T*>(a.delta_raw), bh) + (a.bias ? __ldg(a.bias + h) : 0.f);
+    const float A = head_param(a, a.A, h), D = head_param(a, a.D, h);
+    const float r = IO<T>::load(static_cast<const T*>(a.delta_raw), bh) + head_param(a, a.bias, h);
     const float dl = a.softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
     const float qv = dl * A, dec = ex2(qv * kLog2e), w = A != 0.f ? expm1f(qv) / A : dl;
     float y[kStepRows];
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* sta
             const int p = p0 + k * RW;
             if (p >= a.P) continue;
             float* sp = state + (bh * a.P + p) * a.N + n;
-            if (!one) s[k].load_rw(sp);
+            if (!one && held(p, n)) s[k].load_rw(sp);
             float sv[V];
             s[k].get(sv);
 #pragma unroll
@@ -566,7 +583,7 @@ __global__ void __launch_bounds__(128) heads_step_kernel(HeadsArgs a, float* sta
                 sv[v] = fmaf(dec, sv[v], w * x[k] * Bn[v]);
                 y[k] = fmaf(sv[v], Cn[v], y[k]);
             }
-            store_vec<V>(sp, sv);
+            if (held(p, n)) store_vec<V>(sp, sv);
         }
     }
 #pragma unroll

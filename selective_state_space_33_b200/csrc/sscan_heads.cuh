@@ -11,6 +11,7 @@
 
 #include <cuda_runtime.h>
 
+#include "sscan_check.cuh"
 #include "sscan_host.h"
 #include "sscan_launch.h"
 #include "sscan_math.cuh"
@@ -41,6 +42,14 @@ struct HeadsArgs {
     unsigned int* handed;     // [batch][H][nseg] 1 once that state is there
 };
 
+// Extents of the arrays below, in elements, and head h's entry of a parameter (0 without one).
+__device__ __forceinline__ int64_t state_extent(const HeadsArgs& a) { return a.batch * a.H * a.P * a.N; }
+__device__ __forceinline__ int64_t states_extent(const HeadsArgs& a) { return a.nseg * state_extent(a); }
+__device__ __forceinline__ int64_t segments(const HeadsArgs& a) { return a.batch * a.H * a.nseg; }
+__device__ __forceinline__ float head_param(const HeadsArgs& a, const float* p, int h) {
+    return p && in_range(h, a.H) ? __ldg(p + h) : 0.f;
+}
+
 // Scalars of one chunk's steps, and their running sums (read two at a time, hence the alignment).
 template <int Q>
 struct alignas(16) ChunkScalarsOf {
@@ -65,7 +74,7 @@ __device__ __forceinline__ void chunk_scalars(ChunkScalarsOf<Q>& s, const HeadsA
                                               ChunkSteps* steps = nullptr) {
     constexpr int PER = Q / 32;  // consecutive steps of a lane
     const int lane = threadIdx.x & 31;
-    const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
+    const float A = head_param(a, a.A, h), bias = head_param(a, a.bias, h);
     const T* dr = static_cast<const T*>(a.delta_raw);
     double c[PER];
     float w[PER];
@@ -208,14 +217,14 @@ template <typename T, int COUNT, typename Place>
 static __device__ __noinline__ void state_by_steps(float* S, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
                                             int64_t t1, const float* first) {
     const int grp = h / (a.H / a.G);
-    const float A = __ldg(a.A + h), bias = a.bias ? __ldg(a.bias + h) : 0.f;
+    const float A = head_param(a, a.A, h), bias = head_param(a, a.bias, h);
     unsigned long long todo = 0;
 #pragma unroll 1
     for (int j = 0; j < COUNT; ++j) {
         const int2 at = place(j);
         if (fabsf(S[j]) <= 3.4e38f || at.x >= a.P || at.y >= a.N) continue;
         todo |= 1ull << j;
-        S[j] = first ? first[(int64_t)at.x * a.N + at.y] : 0.f;
+        S[j] = first && in_range((int64_t)at.x * a.N + at.y, (int64_t)a.P * a.N) ? first[(int64_t)at.x * a.N + at.y] : 0.f;
     }
 #pragma unroll 1
     for (int64_t t = t0; t < t1 && todo; ++t) {

@@ -97,22 +97,26 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Loads a P x N fp32 state into its parts, tiles of T ([p][n], zero-padded).
+// Loads the P x N fp32 state at `at` of `states` (of `extent` elements) into its parts, tiles of T ([p][n], zero-padded).
 template <typename T, int NT, typename Each>
-__device__ __forceinline__ void load_state(T* hi, T* lo, T* third, const float* src, int P, int N, int tid, Each each) {
+__device__ __forceinline__ void load_state(T* hi, T* lo, T* third, const float* states, int64_t at, int64_t extent, int P, int N,
+                                           int tid, Each each) {
     constexpr int pitch = HeadsPitch<T, NT>::N;
     for (int i = tid; i < kHeadDim * NT / 4; i += kThreads) {
         const int p = i / (NT / 4), n = (i - p * (NT / 4)) * 4;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (p < P && n < N) {
-            const float* s = src + (int64_t)p * N + n;
+            const float* s = states + at + (int64_t)p * N + n;
+            const int64_t i0 = at + (int64_t)p * N + n;
             if (N % 4 == 0) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(s));
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                if (in_range(i0, extent, 4)) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(s));
+                    v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (n + k < N) v[k] = __ldg(s + k);
+                    if (n + k < N && in_range(i0 + k, extent)) v[k] = __ldg(s + k);
             }
         }
 #pragma unroll
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
 
     for (int h = h_begin; h < h_end; ++h) {
         const int64_t bh = b * a.H + h;
-        const float D = a.D ? __ldg(a.D + h) : 0.f;
+        const float D = head_param(a, a.D, h);
         if (w == 0) chunk_scalars<T>(sm.s, a, b, h, t0, &sm.steps);
         // u, dy and their product's sum
         float dsum = 0.f, ssum = 0.f;
@@ -198,13 +202,13 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             const int64_t at = (bh * a.chunks + c) * a.P * a.N;
             constexpr int PER = kHeadDim * NT / 4 / kThreads;
             float sv[PER][4];
-            load_state<T, NT>(sm.sh, sm.sl, sm.m2, a.states + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
+            load_state<T, NT>(sm.sh, sm.sl, sm.m2, a.states, at, states_extent(a), a.P, a.N, tid, [&](int i, const float (&v)[4]) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     if (i == tid + j * kThreads)
                         for (int e = 0; e < 4; ++e) sv[j][e] = v[e];
             });
-            load_state<T, NT>(sm.rh, sm.rl, sm.m1, k.R + at, a.P, a.N, tid, [&](int i, const float (&v)[4]) {
+            load_state<T, NT>(sm.rh, sm.rl, sm.m1, k.R, at, states_extent(a), a.P, a.N, tid, [&](int i, const float (&v)[4]) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     if (i == tid + j * kThreads)
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
         __syncthreads();
         // the scalars' gradients: one warp, steps 2 lane and 2 lane + 1
         if (w == 0) {
-            const float A = __ldg(a.A + h), end = ex2(sm.s.total * kLog2e);
+            const float A = head_param(a, a.A, h), end = ex2(sm.s.total * kLog2e);
             float ss = 0.f, ds = 0.f;
 #pragma unroll
             for (int i = 0; i < kThreads / 32; ++i) ds += sm.sum[0][i], ss += sm.sum[1][i];
@@ -490,10 +494,11 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             sa = warp_sum(sa);
             sb = warp_sum(sb);
             if (lane == 0) {
-                float* o = k.part + (b * a.chunks + c) * 3 * a.H + h;
-                o[0] = sa;
-                o[a.H] = sb;
-                o[2 * a.H] = ds;
+                const int64_t at = (b * a.chunks + c) * 3 * a.H + h, extent = a.batch * a.chunks * 3 * a.H;
+                float* o = k.part + at;
+                if (in_range(at, extent)) o[0] = sa;
+                if (in_range(at + a.H, extent)) o[a.H] = sb;
+                if (in_range(at + 2 * a.H, extent)) o[2 * a.H] = ds;
             }
         }
         __syncthreads();
@@ -519,8 +524,10 @@ __global__ void __launch_bounds__(kThreads, !Mma<T>::kExact32 && NT <= 64 ? 2 : 
             const int t = i < 2 ? ra : rb, n = 8 * j + 2 * q + (i & 1);
             if (t >= rows || n >= a.N) continue;
             const int64_t at = ((tok + t) * a.G + grp) * a.N + n;
-            if (k.bc) k.bc[(2 * (int64_t)split + wc) * a.batch * a.L * a.G * a.N + at] = bc[j][i];
-            else static_cast<T*>(wc == 0 ? k.dC : k.dB)[at] = from_f32<T>(bc[j][i]);
+            if (k.bc) {
+                const int64_t n_bc = a.batch * a.L * a.G * a.N, to = (2 * (int64_t)split + wc) * n_bc + at;
+                if (in_range(to, 2 * k.splits * n_bc)) k.bc[to] = bc[j][i];
+            } else static_cast<T*>(wc == 0 ? k.dC : k.dB)[at] = from_f32<T>(bc[j][i]);
         }
 }
 
@@ -530,7 +537,7 @@ __global__ void __launch_bounds__(256) heads_bc_kernel(const float* bc, T* dB, T
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= 2 * n) return;
     float s = 0.f;
-    for (int k = 0; k < splits; ++k) s += __ldg(bc + 2 * k * n + i);
+    for (int k = 0; k < splits; ++k) s += in_range(2 * k * n + i, 2 * splits * n) ? __ldg(bc + 2 * k * n + i) : 0.f;
     if (i < n) dC[i] = from_f32<T>(s);
     else dB[i - n] = from_f32<T>(s);
 }
@@ -542,7 +549,7 @@ struct HeadsGradPut {
     __device__ void operator()(int64_t c, float s) const {
         const int64_t k = c / H, h = c - k * H;
         float* to = k == 0 ? dA : k == 1 ? dbias : dD;
-        if (to) to[h] = s;
+        if (to && in_range(h, H)) to[h] = s;
     }
 };
 

@@ -171,7 +171,7 @@ __device__ __noinline__ void rare_outputs(const HeadsArgs& a, const ChunkScalars
                                           unsigned char* zb, int b, int h, int64_t t0, int t, int p0) {
     const bf16 *u = static_cast<const bf16*>(a.u), *B = static_cast<const bf16*>(a.B), *C = static_cast<const bf16*>(a.C);
     const int grp = h / (a.H / a.G);
-    const float e = s.e[t], D = a.D ? __ldg(a.D + h) : 0.f;
+    const float e = s.e[t], D = head_param(a, a.D, h);
     float ya[16], yb[16];
     tmem_load(ya, ya_at);
     tmem_load(yb, yb_at);
@@ -375,7 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const int p = p0 + k;
-            S[k] = first && r < a.N && p < a.P ? first[(int64_t)p * a.N + r] : 0.f;
+            const int64_t at = (int64_t)p * a.N + r;
+            S[k] = first && r < a.N && p < a.P &&
+                           in_range((a.nseg > 1 ? bh * a.nseg + seg : bh) * a.P * a.N + at, a.nseg > 1 ? states_extent(a) : state_extent(a))
+                       ? first[at] : 0.f;
         }
     }
     auto put_state = [&] {  // bf16 S for Ya: row r of [n][p]
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float ya[16], yb[16];
                 tmem_load(ya, tm_row + kColYa + p0);
                 tmem_load(yb, tm_row + kColYb + p0);
-                const float e = sc.e[r], D = a.D ? __ldg(a.D + h) : 0.f;
+                const float e = sc.e[r], D = head_param(a, a.D, h);
                 unsigned char* zb = reinterpret_cast<unsigned char*>(sm.z);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -539,16 +542,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.h_last && seg == a.nseg - 1 && r < a.N) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-                if (p0 + k < a.P) a.h_last[bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
+                if (p0 + k < a.P && in_range(bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r, state_extent(a)))
+                    a.h_last[bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
         }
         work_sync();                           // the last chunk's outputs may leave
     } else {
         if (r < a.N) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-                if (p0 + k < a.P) a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
+                if (p0 + k < a.P && in_range((bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r, states_extent(a)))
+                    a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
         }
-        if (tid == 0) a.decays[bh * a.nseg + seg] = (float)total;
+        if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) a.decays[bh * a.nseg + seg] = (float)total;
     }
     __syncthreads();
     if (w == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols));

@@ -165,6 +165,9 @@ cudaError_t launch_bwd_tiled(const BwdTiledArgs& a, const BwdTiledPtrs& p, int i
 cudaError_t launch_bwd_carry(const BwdTiledArgs& a, cudaStream_t st);
 cudaError_t read_device_error_bwd(unsigned int* value, int clear);
 
+// Debug build: the elements by which its index checks take every array to be shorter.  Synchronous.
+cudaError_t debug_shorten(long long elements);
+
 // Read (and optionally clear) the library's device error word; nonzero means a
 // bounded wait in a kernel gave up.  Synchronous.
 cudaError_t read_device_error(unsigned int* value, int clear);

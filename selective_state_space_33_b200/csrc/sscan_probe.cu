@@ -37,6 +37,12 @@ extern "C" sscan_status sscan_probe_wait_timeout(unsigned int polls, void* strea
                                                                                             : SSCAN_ERR_CUDA;
 }
 
+extern "C" sscan_status sscan_debug_shorten(int64_t elements) {
+    if (elements < 0 || elements > (1 << 20)) return SSCAN_ERR_INVALID_ARG;
+    if (!sscan_debug_bounds()) return SSCAN_ERR_UNSUPPORTED;
+    return sscan::debug_shorten(elements) == cudaSuccess ? SSCAN_OK : SSCAN_ERR_CUDA;
+}
+
 extern "C" sscan_status sscan_probe_layer_wait_timeout(int wait, unsigned int polls, void* stream) {
     if (polls == 0 || polls > (1u << 20)) return SSCAN_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

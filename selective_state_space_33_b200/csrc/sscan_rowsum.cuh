@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "sscan_check.cuh"
+
 namespace sscan {
 
 constexpr int kSumGroups = 32;
@@ -23,7 +25,7 @@ __global__ void __launch_bounds__(32 * kSumGroups) rowsum_kernel(const float* __
     float s = 0.f;
     if (c < cols) {
 #pragma unroll 4
-        for (int64_t r = grp; r < rows; r += kSumGroups) s += __ldg(src + r * cols + c);
+        for (int64_t r = grp; r < rows; r += kSumGroups) s += in_range(r * cols + c, rows * cols) ? __ldg(src + r * cols + c) : 0.f;
     }
     part[grp][lane] = s;
     __syncthreads();

@@ -41,6 +41,9 @@
 namespace sscan {
 
 __device__ unsigned int g_device_error = 0;
+#ifdef SSCAN_DEBUG_BOUNDS
+__device__ long long g_debug_shorten = 0;
+#endif
 
 namespace {
 
@@ -663,6 +666,15 @@ __global__ void wait_probe_kernel(unsigned int polls) {
 cudaError_t launch_wait_probe(unsigned int polls, cudaStream_t st) {
     wait_probe_kernel<<<1, 32, 0, st>>>(polls);
     return cudaGetLastError();
+}
+
+cudaError_t debug_shorten(long long elements) {
+#ifdef SSCAN_DEBUG_BOUNDS
+    return cudaMemcpyToSymbol(g_debug_shorten, &elements, sizeof elements);
+#else
+    (void)elements;
+    return cudaErrorNotSupported;
+#endif
 }
 
 cudaError_t read_device_error(unsigned int* value, int clear) {
