@@ -15,6 +15,7 @@
 #include "sscan_check.cuh"
 #include "sscan_host.h"
 #include "sscan_math.cuh"
+#include "sscan_plan.h"
 #include "sscan_rowsum.cuh"
 #include "sscan_vec.cuh"
 
@@ -396,7 +397,7 @@ sscan_status check_conv(const sscan_conv_problem* p) {
 // 128 per SM), so that small problems spread out and large ones re-read few rows (K-1 per
 // stretch).  8 x 2048 x 1536 bf16: 25.2 us at the 48 this gives, 26.5, 28.0 and 27.4 at 24, 32, 64.
 int64_t conv_fwd_tile(const sscan_conv_problem* p) {
-    const int64_t n = (p->batch * p->seqlen * ((p->dim + 3) / 4) / (148 * 1024) + kAhead - 1) / kAhead * kAhead;
+    const int64_t n = (p->batch * p->seqlen * ((p->dim + 3) / 4) / (kSmCount * 1024) + kAhead - 1) / kAhead * kAhead;
     return n < kAhead ? kAhead : n > 48 ? 48 : n;
 }
 

@@ -42,6 +42,7 @@
 #include "sscan_host.h"
 #include "sscan_launch.h"
 #include "sscan_math.cuh"
+#include "sscan_plan.h"
 #include "sscan_rowsum.cuh"
 #include "sscan_tma.cuh"
 #include "sscan_vec.cuh"
@@ -1030,12 +1031,10 @@ bool gated_map(CUtensorMap* m, const void* base, const GatedArgs& g, int rows) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks that the GPU holds at once; fewer tiles take fewer.
-constexpr int64_t kSms = 148;
-
 template <typename T, int V, bool kTma>
 cudaError_t launch_gated(const GatedArgs& g, bool bwd, cudaStream_t st) {
-    const int64_t all = g.chain.cols * g.chain.tiles, hold = (sizeof(T) == 2 ? 2 : 1) * kSms;
+    // as many blocks as the GPU holds at once; fewer tiles take fewer
+    const int64_t all = g.chain.cols * g.chain.tiles, hold = (sizeof(T) == 2 ? 2 : 1) * kSmCount;
     const unsigned blocks = (unsigned)(all < hold ? all : hold);
     CUtensorMap m[7] = {};
     cudaError_t e;

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "sscan_heads.cuh"
+#include "sscan_plan.h"
 #include "sscan_vec.cuh"
 
 namespace sscan {
@@ -658,7 +659,7 @@ int64_t heads_slots(const HeadsArgs& a, bool bf16) {
         return a.N <= 16 ? Walk<T, 16, kWalkOut>::blocks : a.N <= 32 ? Walk<T, 32, kWalkOut>::blocks
                : a.N <= 64 ? Walk<T, 64, kWalkOut>::blocks : Walk<T, 128, kWalkOut>::blocks;
     };
-    return 148 * (int64_t)(bf16 ? per(__nv_bfloat16{}) : per(float{}));
+    return kSmCount * (int64_t)(bf16 ? per(__nv_bfloat16{}) : per(float{}));
 }
 
 // Segments of a forward pass.  With fewer (batch, head) pairs than SMs a sequence is split into as
@@ -669,7 +670,7 @@ int64_t heads_slots(const HeadsArgs& a, bool bf16) {
 void plan_segments(HeadsArgs& a, int64_t slots, int64_t least) {
     const int64_t bh = a.batch * a.H;
     int64_t nseg = 1;
-    if (bh < 148) {
+    if (bh < kSmCount) {
         nseg = slots / bh;
         if (nseg > (a.chunks + least - 1) / least) nseg = (a.chunks + least - 1) / least;
         if (nseg < 2) nseg = 1;
@@ -696,7 +697,7 @@ void plan_heads(HeadsArgs& a, bool bf16, bool tc) {
         a.nseg = (a.chunks + kHandedChunks - 1) / kHandedChunks;
         return;
     }
-    plan_segments(a, tc ? 148 : heads_slots(a, bf16), tc ? 2 : 4);
+    plan_segments(a, tc ? kSmCount : heads_slots(a, bf16), tc ? 2 : 4);
 }
 
 size_t split_bytes(const HeadsArgs& a) {

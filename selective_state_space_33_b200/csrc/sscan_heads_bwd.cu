@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "sscan_heads.cuh"
+#include "sscan_plan.h"
 #include "sscan_rowsum.cuh"
 #include "sscan_vec.cuh"
 
@@ -580,7 +581,7 @@ cudaError_t bwd_n(const HeadsBwdArgs& k, cudaStream_t st) {
 // for about four per SM.
 void plan_splits(const sscan_heads_problem* p, int64_t chunks, int* splits, int* per) {
     const int64_t hg = p->heads / p->groups, base = chunks * p->batch * p->groups;
-    int64_t n = (4 * 148 + base - 1) / base;
+    int64_t n = (4 * kSmCount + base - 1) / base;
     if (n > hg) n = hg;
     const int64_t each = (hg + n - 1) / n;
     *per = (int)each;
