@@ -443,28 +443,27 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
     bool lost = false;
 #pragma unroll
     for (int j = 0; j < NTL; ++j) lost = lost || not_finite(S[j]);
-    if (!kRev && lost) {
-        float v[4 * NTL];
-#pragma unroll
-        for (int j = 0; j < 4 * NTL; ++j) v[j] = S[j / 4][j % 4];
+    auto mend = [&](float* dest) {
+        if (kRev || !lost) return;
         auto place = [p = p0 + g, m = n0 + 2 * q](int j) { return make_int2(p + (j >> 1 & 1) * 8, m + 8 * (j >> 2) + (j & 1)); };
         const int64_t end = c1 * kQ;
-        state_by_steps<T, 4 * NTL>(v, place, a, b, h, c0 * kQ, end < a.L ? end : a.L, entering());
-#pragma unroll
-        for (int j = 0; j < 4 * NTL; ++j) S[j / 4][j % 4] = v[j];
-    }
+        state_by_steps<T, 4 * NTL>(dest, place, a, b, h, c0 * kQ, end < a.L ? end : a.L, entering());
+    };
     if (MODE == kWalkOut) {
         if (a.h_last && seg == a.nseg - 1) {
             float* o = a.h_last + bh * a.P * a.N;
             each_state([&](float& v, int64_t at) {
                 if (in_range(bh * a.P * a.N + at, state_extent(a))) o[at] = v;
             });
+            mend(o);
         }
         if (a.ticket && seg < a.nseg - 1) {
             float* o = a.states + (bh * a.nseg + seg) * a.P * a.N;
             each_state([&](float& v, int64_t at) {
                 if (in_range((bh * a.nseg + seg) * a.P * a.N + at, states_extent(a))) __stcg(o + at, v);
             });
+            mend(o);
+            __syncwarp();
             __threadfence();
             product_sync<kWork>();
             if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) hand_on(a.handed + bh * a.nseg + seg);
@@ -474,6 +473,7 @@ __global__ void __launch_bounds__(Walk<T, NT, MODE>::threads, Walk<T, NT, MODE>:
         each_state([&](float& v, int64_t at) {
             if (in_range((bh * a.nseg + seg) * a.P * a.N + at, states_extent(a))) o[at] = v;
         });
+        mend(o);
         if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) a.decays[bh * a.nseg + seg] = (float)total;
     }
 }

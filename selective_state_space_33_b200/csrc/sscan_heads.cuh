@@ -209,23 +209,28 @@ template <typename T, int NT> struct HeadsPitch {
     static constexpr int Q = kQ + Mma<T>::PAD;
 };
 
-// A thread's elements S[j], j < COUNT <= 64, of the state after steps t0 .. t1 - 1 of (b, h), at (p, n) = place(j):
-// those that are not finite are taken again from the state `first` before t0 (null: zero), step by
-// step.  A chunk's products split their operands in parts, and an infinity in one of them is not a number
-// there, where the recurrence has an infinity.  An infinity is not decayed here, since exp(q) may underflow.
+// A thread's elements (p, n) = place(j), j < COUNT <= 64, of the state after steps t0 .. t1 - 1 of (b, h), as it
+// has just stored them to `dest`: those that are not finite are taken again from the state `first` before t0
+// (null: zero), step by step.  A chunk's products split their operands in parts, and an infinity in one of
+// them is not a number there, where the recurrence has an infinity.  An infinity is not decayed here, since
+// exp(q) may underflow.
 template <typename T, int COUNT, typename Place>
-static __device__ __noinline__ void state_by_steps(float* S, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
-                                            int64_t t1, const float* first) {
+static __device__ __noinline__ void state_by_steps(float* dest, Place place, const HeadsArgs& a, int64_t b, int h, int64_t t0,
+                                                   int64_t t1, const float* first) {
     const int grp = h / (a.H / a.G);
+    const int64_t extent = (int64_t)a.P * a.N;
     const float A = head_param(a, a.A, h), bias = head_param(a, a.bias, h);
-    unsigned long long todo = 0;
+    float S[COUNT];
+    unsigned long long redo = 0;
 #pragma unroll 1
     for (int j = 0; j < COUNT; ++j) {
         const int2 at = place(j);
-        if (fabsf(S[j]) <= 3.4e38f || at.x >= a.P || at.y >= a.N) continue;
-        todo |= 1ull << j;
-        S[j] = first && in_range((int64_t)at.x * a.N + at.y, (int64_t)a.P * a.N) ? first[(int64_t)at.x * a.N + at.y] : 0.f;
+        const int64_t i = (int64_t)at.x * a.N + at.y;
+        if (at.x >= a.P || at.y >= a.N || !in_range(i, extent) || fabsf(__ldcg(dest + i)) <= 3.4e38f) continue;
+        redo |= 1ull << j;
+        S[j] = first ? __ldcg(first + i) : 0.f;
     }
+    unsigned long long todo = redo;
 #pragma unroll 1
     for (int64_t t = t0; t < t1 && todo; ++t) {
         const int64_t tok = b * a.L + t;
@@ -241,6 +246,12 @@ static __device__ __noinline__ void state_by_steps(float* S, Place place, const 
             S[j] = fmaf(fabsf(S[j]) > 3.4e38f ? 1.f : e, S[j], x);
             if (S[j] != S[j]) todo &= ~(1ull << j);  // and it stays so
         }
+    }
+#pragma unroll 1
+    for (; redo; redo &= redo - 1) {
+        const int j = __ffsll((long long)redo) - 1;
+        const int2 at = place(j);
+        __stcg(dest + (int64_t)at.x * a.N + at.y, S[j]);
     }
 }
 

@@ -208,13 +208,14 @@ __device__ __forceinline__ const float* entering_state(const HeadsArgs& a, int64
 // state_by_steps of a working thread's 16 elements over the block's segment; everything it needs is worked out
 // anew, which costs the usual path no registers.
 template <bool kOut>
-__device__ __noinline__ void segment_by_steps(float* S, const HeadsArgs& a) {
+__device__ __noinline__ void segment_by_steps(const HeadsArgs& a) {
     const int64_t seg = blockIdx.x / a.H, b = blockIdx.y;
     const int h = (int)(blockIdx.x - seg * a.H), w = threadIdx.x >> 5;
     const int row = 32 * (w & 3) + (threadIdx.x & 31), p0 = 16 * (w >> 2);
-    const int64_t t0 = seg * a.seg_chunks * kTcQ, end = t0 + a.seg_chunks * kTcQ;
-    state_by_steps<bf16, 16>(S, [p0, row](int k) { return make_int2(p0 + k, row); }, a, b, h, t0, end < a.L ? end : a.L,
-                             entering_state<kOut>(a, b * a.H + h, seg));
+    const int64_t t0 = seg * a.seg_chunks * kTcQ, end = t0 + a.seg_chunks * kTcQ, bh = b * a.H + h;
+    float* dest = kOut ? a.h_last + bh * a.P * a.N : a.states + (bh * a.nseg + seg) * a.P * a.N;
+    state_by_steps<bf16, 16>(dest, [p0, row](int k) { return make_int2(p0 + k, row); }, a, b, h, t0, end < a.L ? end : a.L,
+                             entering_state<kOut>(a, bh, seg));
 }
 
 // kOut: outputs, from the state entering the segment; else the segment's end state from zero.
@@ -529,22 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async();
         }
     }
-    // an infinity or a NaN stays in the state once it is there
-    if (not_finite(S)) {
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = S[k];
-        segment_by_steps<kOut>(v, a);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) S[k] = v[k];
-    }
+    // (an infinity or a NaN stays in the state once it is there)
     if (kOut) {
         if (a.h_last && seg == a.nseg - 1 && r < a.N) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 if (p0 + k < a.P && in_range(bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r, state_extent(a)))
                     a.h_last[bh * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
+            if (not_finite(S)) segment_by_steps<kOut>(a);
         }
+        __syncwarp();
         work_sync();                           // the last chunk's outputs may leave
     } else {
         if (r < a.N) {
@@ -552,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 16; ++k)
                 if (p0 + k < a.P && in_range((bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r, states_extent(a)))
                     a.states[(bh * a.nseg + seg) * a.P * a.N + (int64_t)(p0 + k) * a.N + r] = S[k];
+            if (not_finite(S)) segment_by_steps<kOut>(a);
         }
         if (tid == 0 && in_range(bh * a.nseg + seg, segments(a))) a.decays[bh * a.nseg + seg] = (float)total;
     }
