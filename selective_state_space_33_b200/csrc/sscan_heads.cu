@@ -10,7 +10,7 @@
 // fp32 quantity into the state (u or B scaled by f) goes in as three bf16 parts, the state
 // read by the outputs as two, and the entries of M are rounded to bf16 once, an error of the
 // same size as the rounding of the result.
-// 8 x 2048, 80 heads of 64 channels, 16 states, bf16 with gate: 244 us (508 MB, 2.1 TB/s); issue
+// 8 x 2048, 80 heads of 64 channels, 16 states, bf16 with gate: 243 us (508 MB, 2.1 TB/s); issue
 // slots 54% busy with three blocks per SM, no pipe above 30%: a chunk's steps wait for one another.
 #include <cuda_runtime.h>
 
@@ -665,8 +665,10 @@ int64_t heads_slots(const HeadsArgs& a, bool bf16) {
 // Segments of a forward pass.  With fewer (batch, head) pairs than SMs a sequence is split into as
 // many segments, of at least four chunks, as fill the GPU once: a block more than it holds would
 // wait for a whole segment (65536 steps, 24 heads: with 32 states, where 444 blocks fit, 18 segments,
-// 432 blocks, 535 us, 27 segments 673 us; with 128 states on tcgen05, where 148 fit, 6 segments 640 us,
-// 9 segments 840 us).
+// 432 blocks, 530 us, 27 segments 682 us; with 128 states on tcgen05, where 148 fit, 6 segments 621 us,
+// 9 segments 819 us).  From one pair per SM on it is not split, which leaves slots empty up to where segments are
+// handed on: 16 states, 16384 steps, 147 / 148 / 160 / 220 pairs take 587 / 859 / 1000 / 1019 us, and with a split up to
+// half the slots 587 / 586 / 849 / 876 us.
 void plan_segments(HeadsArgs& a, int64_t slots, int64_t least) {
     const int64_t bh = a.batch * a.H;
     int64_t nseg = 1;

@@ -18,9 +18,9 @@
 // 8e-5 off where the same sums in fp32 lose 1e-6), so everything that feeds them (H, S C, R B)
 // takes its inexact factor as three bf16 parts, 24 bits; M1 and the factors of the products
 // that end in bf16 are rounded once.
-// 8 x 2048, 24 heads of 64 channels, 64 states, bf16 with gate: 477 us; two blocks of eight warps per SM,
-// issue slots about a third busy, the rest the latency of nine products that follow one another
-// (sixteen warps of 64 registers were tried and were slower).
+// 8 x 2048, 24 heads of 64 channels, 64 states, bf16 with gate: 480 us; two blocks of eight warps per SM,
+// issue slots about a third busy, the rest the latency of nine products that follow one another, and of what
+// 128 registers per thread do not hold (528 bytes of spills; sixteen warps of 64 registers were tried and were slower).
 #include <cuda_runtime.h>
 
 #include "sscan_heads.cuh"

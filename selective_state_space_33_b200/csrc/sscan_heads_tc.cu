@@ -4,9 +4,9 @@
 // With 128 states the chunk's products are 2 x 128 x (128 + 3 x 64 + 64 + 64) x 128 operations against 48 KB
 // of traffic; as mma.sync they kept eight warps loading fragments (1470 us at 65536 steps, 24 heads, 128
 // states, issue slots 45% busy, tensor pipe under 40%).  Here one thread issues them from
-// shared memory and tensor memory, and the warps only do what is elementwise: 640 us, about
+// shared memory and tensor memory, and the warps only do what is elementwise: 621 us, about
 // 72% of it the output pass and 27% the pass over the segments' states.  What is left is the order of a chunk's
-// steps with one block per SM (output pass: issue slots 37%, tensor pipe 18% busy); barriers that keep the
+// steps with one block per SM (output pass: issue slots 39%, tensor pipe 19% busy); barriers that keep the
 // working warps in step are faster than mbarriers that let them drift (815 against 764 us at
 // that stage: drifting warps miss the instruction cache).
 //
