@@ -25,7 +25,7 @@
 // stored and polled whole, so no fence or second round trip is needed.
 //
 // 8 x 2048 x 5120 bf16 forward: 126 us, 5.3 TB/s (82% of the measured copy bandwidth), issue slots
-// 61% busy; 8 x 2048 x 1536: forward and backward 138 us, a third and two thirds; 131072 x 1536: 568 us, there the
+// 61% busy; 8 x 2048 x 1536: forward and backward 139 us, a third and two thirds; 131072 x 1536: 573 us, there the
 // tiles of a column that run at the same time wait for each other's maps.
 //
 // Per element the forward moves 4 I/O elements against 4 special-function operations (5 where a
@@ -127,28 +127,39 @@ __device__ __forceinline__ void decay2(float2 s, float2& a, float2& om) {
     om = mul2(e, fma2(e, splat(-1.f), splat(2.f)));
 }
 
-// sigmoid(x + bias) of both gates for two elements, nbias = -log2(e) bias: 1 / D with D = 1 + 2^q,
-// q = nbias - log2(e) x.  Both gates come from one reciprocal, 1 / D_r = D_i / (D_r D_i), which holds while
-// the product is in fp32's range.  The products are added to `shut`: where that is not below kShut (a gate is as
-// good as closed, or not a number), the caller takes gate2 instead.
-constexpr float kShut = 0x1p120f;
+// min(x, most) that keeps a NaN
+__device__ __forceinline__ float min_nan(float x, float most) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+    return y;
+}
 
-__device__ __forceinline__ void gates2(float2 xr, float2 xi, float2 nbr, float2 nbi, float2& r, float2& i, float2& shut) {
+// a b, with results below 2^-126 as 0
+__device__ __forceinline__ float2 mul2_ftz(float2 a, float2 b) {
+    float2 y;
+    asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.ftz.f32x2 y, a, b;\n\t"
+        "mov.b64 {%0, %1}, y;\n\t}"
+        : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
+
+// sigmoid(x + bias) of both gates for two elements: 1 / D with D = 1 + 2^q, q = -log2(e) (x + bias).  Both come
+// from one reciprocal, 1 / D_r = D_i / (D_r D_i), with D_i scaled by 2^-kShift (nbi = -log2(e) bias - kShift, which
+// leaves 2^q its normal range below 1), so that the product is in fp32's range while one gate is open.  A gate
+// goes down to 2^-126, then to 0: from q = 127 on, where q is held, and for an x of -inf, it is exactly that, and the
+// other gate is as it would be.  (Both are 0 where their product is below 2^-226.)
+constexpr float kShift = 100.f;
+
+__device__ __forceinline__ void gates2(float2 xr, float2 xi, float2 nbr, float2 nbi, float2& r, float2& i) {
     const float2 qr = fma2(xr, splat(-kLog2e), nbr), qi = fma2(xi, splat(-kLog2e), nbi);
-    const float2 dr = add2(make_float2(ex2(qr.x), ex2(qr.y)), splat(1.f));
-    const float2 di = add2(make_float2(ex2(qi.x), ex2(qi.y)), splat(1.f)), p = mul2(dr, di);
-    shut = add2(shut, p);
+    const float2 er = make_float2(ex2(min_nan(qr.x, 127.f)), ex2(min_nan(qr.y, 127.f)));
+    const float2 ei = make_float2(ex2(min_nan(qi.x, 127.f - kShift)), ex2(min_nan(qi.y, 127.f - kShift)));
+    const float2 dr = add2(er, splat(1.f)), di = add2(ei, splat(0x1p-100f)), p = mul2(dr, di);
     const float2 rp = make_float2(rcp(p.x), rcp(p.y));
-    r = mul2(di, rp);
-    i = mul2(dr, rp);
+    r = mul2_ftz(di, rp);
+    i = mul2_ftz(mul2(dr, splat(0x1p-100f)), rp);
 }
-
-// And of any x, each by a reciprocal of its own, which goes down to 2^-126, and to 0 for an x of -inf.
-__device__ __forceinline__ float2 gate2(float2 x, float2 nbias) {
-    const float2 q = fma2(x, splat(-kLog2e), nbias);
-    const float2 d = add2(make_float2(ex2(q.x), ex2(q.y)), splat(1.f));
-    return make_float2(rcp(d.x), rcp(d.y));
-}
+__device__ __forceinline__ float gate_bias(const float* bias, int64_t d) { return bias ? -kLog2e * __ldg(bias + d) : 0.f; }
 
 // rate * softplus(Lam), once per channel of a block
 __device__ __forceinline__ float decay_rate(float lam, float rate) {
@@ -367,21 +378,18 @@ __device__ __forceinline__ float2 pair_of(const T* rows, int k) {
 __device__ __forceinline__ void hold_loads() { asm volatile("" ::: "memory"); }
 
 // The gates and the recurrence's terms for the STEPS x V elements of a thread's column of a tile,
-// two at a time: the V = 2 channels of a step, or two steps of the one channel.  False when a gate was out
-// of gates2's range.
+// two at a time: the V = 2 channels of a step, or two steps of the one channel.
 template <typename T, int V, int STEPS, bool kAny, typename Out>
-__device__ __forceinline__ bool gate_terms(float2 c, float2 na, float2 ni, const T* ar, const T* ir, const T* u, Out out) {
-    float2 shut = splat(0.f);
+__device__ __forceinline__ void gate_terms(float2 c, float2 na, float2 ni, const T* ar, const T* ir, const T* u, Out out) {
 #pragma unroll
     for (int k = 0; k < STEPS; k += 3 - V) {
         if (k % 4 == 0) hold_loads();
         float2 r, i, a, om;
-        gates2(pair_of<T, V>(ar, k), pair_of<T, V>(ir, k), na, ni, r, i, shut);
+        gates2(pair_of<T, V>(ar, k), pair_of<T, V>(ir, k), na, ni, r, i);
         decay2<kAny>(mul2(c, r), a, om);
         const float2 m = mul2(om, rsqrt2(om));
         out(k, a, mul2(mul2(m, i), pair_of<T, V>(u, k)), r, i);
     }
-    return shut.x < kShut && shut.y < kShut;
 }
 
 template <int V, int STEPS>
@@ -389,68 +397,6 @@ __device__ __forceinline__ void set_pair(float (&v)[STEPS][V], int k, float2 x) 
     v[k][0] = x.x;
     if constexpr (V == 2) v[k][1] = x.y;
     else v[k + 1][0] = x.y;
-}
-
-// Puts the terms of the elements with a gate out of gates2's range (and of no others) into [STEPS][V] arrays;
-// r and i may be null.  A function of its own, on memory of its own: inlined, it would cost the kernels
-// registers that they do not have (568 bytes of spills, 581 -> 1012 us at 131072 x 1536).
-template <typename T, int V, int STEPS>
-__device__ __noinline__ void shut_terms(float2 c, float2 na, float2 ni, const T* ar, const T* ir, const T* u, float* a,
-                                        float* x, float* r, float* i) {
-#pragma unroll 1
-    for (int k = 0; k < STEPS; k += 3 - V) {
-        const float2 xr = pair_of<T, V>(ar, k), xi = pair_of<T, V>(ir, k), pr = gate2(xr, na), pi = gate2(xi, ni);
-        float2 pa, om, unused, p = splat(0.f);
-        gates2(xr, xi, na, ni, unused, unused, p);
-        decay2<true>(mul2(c, pr), pa, om);
-        const float2 px = mul2(mul2(mul2(om, rsqrt2(om)), pi), pair_of<T, V>(u, k));
-        if (!(p.x < kShut)) {
-            a[k * V] = pa.x, x[k * V] = px.x;
-            if (r) r[k * V] = pr.x, i[k * V] = pi.x;
-        }
-        if (!(p.y < kShut)) {
-            a[k * V + 1] = pa.y, x[k * V + 1] = px.y;
-            if (r) r[k * V + 1] = pr.y, i[k * V + 1] = pi.y;
-        }
-    }
-}
-
-// The terms of a thread's column of a tile.  r <= 1, so a rate below 1/4 keeps every s of the warp there; returns
-// whether some may not be.
-template <typename T, int V, int STEPS, bool kGates>
-__device__ __forceinline__ bool tile_terms(float2 c, float2 na, float2 ni, const T* ar, const T* ir, const T* u,
-                                           float (&a)[STEPS][V], float (&x)[STEPS][V],
-                                           float (&r)[kGates ? STEPS : 1][V], float (&i)[kGates ? STEPS : 1][V]) {
-    auto out = [&](int k, float2 pa, float2 px, float2 pr, float2 pi) {
-        set_pair<V, STEPS>(a, k, pa);
-        set_pair<V, STEPS>(x, k, px);
-        if constexpr (kGates) {
-            set_pair<V, STEPS>(r, k, pr);
-            set_pair<V, STEPS>(i, k, pi);
-        }
-    };
-    const bool any = __any_sync(0xffffffffu, !(c.x < 0.25f && c.y < 0.25f));
-    const bool done = any ? gate_terms<T, V, STEPS, true>(c, na, ni, ar, ir, u, out)
-                          : gate_terms<T, V, STEPS, false>(c, na, ni, ar, ir, u, out);
-    if (!done) {
-        float t[kGates ? 4 : 2][STEPS * V];
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                t[0][k * V + v] = a[k][v], t[1][k * V + v] = x[k][v];
-                if constexpr (kGates) t[2][k * V + v] = r[k][v], t[3][k * V + v] = i[k][v];
-            }
-        shut_terms<T, V, STEPS>(c, na, ni, ar, ir, u, t[0], t[1], kGates ? t[2] : nullptr, kGates ? t[3] : nullptr);
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                a[k][v] = t[0][k * V + v], x[k][v] = t[1][k * V + v];
-                if constexpr (kGates) r[k][v] = t[2][k * V + v], i[k][v] = t[3][k * V + v];
-            }
-    }
-    return any;
 }
 
 // Starts a tile's inputs on their way to buffer `buf`: one thread, by TMA.
@@ -564,14 +510,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
-            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+            nab[v] = live && in_range(d + v, g.D) ? gate_bias(g.a_bias, d + v) : 0.f;
+            nib[v] = (live && in_range(d + v, g.D) ? gate_bias(g.i_bias, d + v) : 0.f) - kShift;
         }
         const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
         const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
         float a[S][V], x[S][V];
-        float unused[1][V];
-        tile_terms<T, V, S, false>(c, na, ni, ar, ir, u, a, x, unused, unused);
+        auto out = [&](int k, float2 pa, float2 px, float2, float2) {
+            set_pair<V, S>(a, k, pa);
+            set_pair<V, S>(x, k, px);
+        };
+        // r <= 1, so a rate below 1/4 keeps every s of the warp there
+        if (__any_sync(0xffffffffu, !(c.x < 0.25f && c.y < 0.25f))) gate_terms<T, V, S, true>(c, na, ni, ar, ir, u, out);
+        else gate_terms<T, V, S, false>(c, na, ni, ar, ir, u, out);
         if (t0 + S > g.L) {  // past the end: the identity map
 #pragma unroll
             for (int k = 0; k < S; ++k)
@@ -751,8 +702,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V], h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
-            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
+            nab[v] = live && in_range(d + v, g.D) ? gate_bias(g.a_bias, d + v) : 0.f;
+            nib[v] = (live && in_range(d + v, g.D) ? gate_bias(g.i_bias, d + v) : 0.f) - kShift;
             const int64_t at = (b * g.chain.tiles + j) * g.D + d + v;
             h[v] = live && in_range(at, g.batch * g.chain.tiles * g.D) ? __ldg(g.ckpt_in + at) : 0.f;
         }
@@ -769,7 +720,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
         const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
         float a[S][V], x[S][V], r[S][V], i[S][V];
-        const bool any = tile_terms<T, V, S, true>(c, na, ni, ar, ir, u, a, x, r, i);
+        auto out = [&](int k, float2 pa, float2 px, float2 pr, float2 pi) {
+            set_pair<V, S>(a, k, pa);
+            set_pair<V, S>(x, k, px);
+            set_pair<V, S>(r, k, pr);
+            set_pair<V, S>(i, k, pi);
+        };
+        const bool any = __any_sync(0xffffffffu, !(c.x < 0.25f && c.y < 0.25f));
+        if (any) gate_terms<T, V, S, true>(c, na, ni, ar, ir, u, out);
+        else gate_terms<T, V, S, false>(c, na, ni, ar, ir, u, out);
         // past the end dout is zero and so is every adjoint: those steps' terms are zeros by themselves
         float A[V], H[V], E[V];
 #pragma unroll
@@ -891,14 +850,12 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
     for (int v = 0; v < V; v += 2) {
         // V = 1 computes its one element twice
         const int v1 = V == 1 ? 0 : v + 1;
-        float2 r, i, a, om, nab = splat(0.f), nib = splat(0.f);
-        if (g.a_bias && params) nab = make_float2(-kLog2e * __ldg(g.a_bias + d + v), -kLog2e * __ldg(g.a_bias + d + v1));
-        if (g.i_bias && params) nib = make_float2(-kLog2e * __ldg(g.i_bias + d + v), -kLog2e * __ldg(g.i_bias + d + v1));
+        float2 r, i, a, om, nab = splat(0.f), nib = splat(-kShift);
+        if (params) nab = make_float2(gate_bias(g.a_bias, d + v), gate_bias(g.a_bias, d + v1));
+        if (params) nib = make_float2(gate_bias(g.i_bias, d + v) - kShift, gate_bias(g.i_bias, d + v1) - kShift);
         const float2 c = !params ? splat(0.f)
                                  : make_float2(decay_rate(__ldg(g.Lam + d + v), g.rate), decay_rate(__ldg(g.Lam + d + v1), g.rate));
-        const float2 xr = make_float2(ar[v], ar[v1]), xi = make_float2(ir[v], ir[v1]);
-        r = gate2(xr, nab);
-        i = gate2(xi, nib);
+        gates2(make_float2(ar[v], ar[v1]), make_float2(ir[v], ir[v1]), nab, nib, r, i);
         decay2<true>(mul2(c, r), a, om);
         const float2 m = mul2(om, rsqrt2(om));
         const float2 hn = fma2(a, make_float2(h[v], h[v1]), mul2(mul2(m, i), make_float2(u[v], u[v1])));

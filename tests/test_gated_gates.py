@@ -158,3 +158,30 @@ def test_one_extreme_gate_changes_nothing_else(cuda_device, io, D, name, value):
     same[1, 150:, 3] = False
     assert torch.equal(out[same], clean[same])
     assert bool(torch.isnan(out[1, 150:, 3]).all()) == (value != value) and not torch.isnan(out[same]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_both_gates_at_every_extreme(cuda_device, io, shift):
+    """One token, every pair of raw values from -inf to inf; by two channels per lane, or one (an odd start)."""
+    values = torch.tensor([-float("inf"), -200.0, -90.0, -87.5, -75.0, -60.0, -42.0, -20.0, 0.0, 20.0, 90.0, float("inf")])
+    a, i = (v.flatten() for v in torch.meshgrid(values, values, indexing="ij"))
+    dt = R.DTYPES[io]
+    x = {"u": torch.full((1, 1, a.numel()), 2.0).to(dt), "a_raw": a.to(dt)[None, None], "i_raw": i.to(dt)[None, None],
+         "Lam": torch.full((a.numel(),), -2.0), "h0": torch.zeros(1, a.numel())}
+    x = {k: v.to(cuda_device) for k, v in x.items()}
+    ref = R.gated(**{k: R.d64(v) for k, v in x.items()})[0]
+    if shift:
+        x.update({k: R.shifted(x[k]) for k in ("u", "a_raw", "i_raw")})
+    out, last = sb.sscan_gated_fwd(**x, return_last_state=True)
+    state = x["h0"].clone()
+    step = sb.sscan_gated_step(x["u"][:, 0], x["a_raw"][:, 0], x["i_raw"][:, 0], x["Lam"], state)
+    # x = m i u in a few roundings; a gate below 2^-126 is 0, as are two whose product is below 2^-226, and sqrt(2 c r) i u with
+    # either left out is below 2^-61 (r = 2^-126 alone) or 2^-98
+    for got in (last, state):
+        assert ((R.d64(got) - ref[:, 0]).abs() <= 64 * EPS * ref[:, 0].abs() + 2.0 ** -61).all()
+        assert (got[0, i.to(cuda_device) == -float("inf")] == 0).all() and (got[0, a.to(cuda_device) == -float("inf")] == 0).all()
+    half = R.HALF_STEP[dt]
+    assert ((R.d64(out) - ref).abs() <= (64 * EPS + half) * ref.abs() + 2.0 ** -61).all()
+    assert torch.equal(step, state.to(dt))
