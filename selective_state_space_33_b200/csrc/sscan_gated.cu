@@ -25,11 +25,11 @@
 // stored and polled whole, so no fence or second round trip is needed.
 //
 // 8 x 2048 x 5120 bf16 forward: 126 us, 5.3 TB/s (82% of the measured copy bandwidth), issue slots
-// 61% busy; 8 x 2048 x 1536: forward and backward 139 us, a third and two thirds; 131072 x 1536: 573 us, there the
+// 63% busy; 8 x 2048 x 1536: forward and backward 139 us, a third and two thirds; 131072 x 1536: 573 us, there the
 // tiles of a column that run at the same time wait for each other's maps.
 //
 // Per element the forward moves 4 I/O elements against 4 special-function operations (5 where a
-// channel's decay can pass exp(-1/4)) and 32 issued instructions; two elements, V = 2
+// channel's decay can pass exp(-1/4)) and 34 issued instructions; two elements, V = 2
 // channels or two steps, share each packed fp32 instruction.
 #include <cuda.h>
 #include <cuda_runtime.h>
