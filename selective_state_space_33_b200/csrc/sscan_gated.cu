@@ -127,10 +127,10 @@ __device__ __forceinline__ void decay2(float2 s, float2& a, float2& om) {
     om = mul2(e, fma2(e, splat(-1.f), splat(2.f)));
 }
 
-// min(x, most) that keeps a NaN
-__device__ __forceinline__ float min_nan(float x, float most) {
+// min(x, 127) that keeps a NaN
+__device__ __forceinline__ float min_nan(float x) {
     float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(127.f));
     return y;
 }
 
@@ -143,23 +143,20 @@ __device__ __forceinline__ float2 mul2_ftz(float2 a, float2 b) {
     return y;
 }
 
-// sigmoid(x + bias) of both gates for two elements: 1 / D with D = 1 + 2^q, q = -log2(e) (x + bias).  Both come
-// from one reciprocal, 1 / D_r = D_i / (D_r D_i), with D_i scaled by 2^-kShift (nbi = -log2(e) bias - kShift, which
-// leaves 2^q its normal range below 1), so that the product is in fp32's range while one gate is open.  A gate
-// goes down to 2^-126, then to 0: from q = 127 on, where q is held, and for an x of -inf, it is exactly that, and the
-// other gate is as it would be.  (Both are 0 where their product is below 2^-226.)
-constexpr float kShift = 100.f;
-
+// sigmoid(x + bias) of both gates for two elements: 1 / D with D = 1 + 2^q, q = nbias - log2(e) x, nbias =
+// -log2(e) bias.  Both come from one reciprocal, 1 / D_r = D_i / (D_r D_i), with D_i scaled by 2^-100, so that the
+// product is in fp32's range while one gate is open.  (The exponent itself is not shifted: its rounding would be that
+// of a number near 100.)  A gate goes down to 2^-126, then to 0: from q = 127 on, where q is held, and for an x
+// of -inf, it is exactly that, and the other gate is as it would be.  Both are 0 where their product is below 2^-226.
 __device__ __forceinline__ void gates2(float2 xr, float2 xi, float2 nbr, float2 nbi, float2& r, float2& i) {
-    const float2 qr = fma2(xr, splat(-kLog2e), nbr), qi = fma2(xi, splat(-kLog2e), nbi);
-    const float2 er = make_float2(ex2(min_nan(qr.x, 127.f)), ex2(min_nan(qr.y, 127.f)));
-    const float2 ei = make_float2(ex2(min_nan(qi.x, 127.f - kShift)), ex2(min_nan(qi.y, 127.f - kShift)));
-    const float2 dr = add2(er, splat(1.f)), di = add2(ei, splat(0x1p-100f)), p = mul2(dr, di);
+    const float2 qr = fma2(xr, splat(-kLog2e), nbr), qi = fma2(xi, splat(-kLog2e), nbi), scale = splat(0x1p-100f);
+    const float2 er = make_float2(ex2(min_nan(qr.x)), ex2(min_nan(qr.y)));
+    const float2 ei = make_float2(ex2(min_nan(qi.x)), ex2(min_nan(qi.y)));
+    const float2 dr = add2(er, splat(1.f)), di = fma2(ei, scale, scale), p = mul2(dr, di);
     const float2 rp = make_float2(rcp(p.x), rcp(p.y));
     r = mul2_ftz(di, rp);
-    i = mul2_ftz(mul2(dr, splat(0x1p-100f)), rp);
+    i = mul2_ftz(mul2(dr, scale), rp);
 }
-__device__ __forceinline__ float gate_bias(const float* bias, int64_t d) { return bias ? -kLog2e * __ldg(bias + d) : 0.f; }
 
 // rate * softplus(Lam), once per channel of a block
 __device__ __forceinline__ float decay_rate(float lam, float rate) {
@@ -510,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && in_range(d + v, g.D) ? gate_bias(g.a_bias, d + v) : 0.f;
-            nib[v] = (live && in_range(d + v, g.D) ? gate_bias(g.i_bias, d + v) : 0.f) - kShift;
+            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
         }
         const float2 c = make_float2(sm.c.rate[buf][lv], sm.c.rate[buf][lv + V - 1]);
         const float2 na = make_float2(nab[0], nab[V - 1]), ni = make_float2(nib[0], nib[V - 1]);
@@ -702,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
         float nab[V], nib[V], h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            nab[v] = live && in_range(d + v, g.D) ? gate_bias(g.a_bias, d + v) : 0.f;
-            nib[v] = (live && in_range(d + v, g.D) ? gate_bias(g.i_bias, d + v) : 0.f) - kShift;
+            nab[v] = live && g.a_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.a_bias + d + v) : 0.f;
+            nib[v] = live && g.i_bias && in_range(d + v, g.D) ? -kLog2e * __ldg(g.i_bias + d + v) : 0.f;
             const int64_t at = (b * g.chain.tiles + j) * g.D + d + v;
             h[v] = live && in_range(at, g.batch * g.chain.tiles * g.D) ? __ldg(g.ckpt_in + at) : 0.f;
         }
@@ -850,9 +847,9 @@ __global__ void __launch_bounds__(128) gated_step_kernel(GatedArgs g) {
     for (int v = 0; v < V; v += 2) {
         // V = 1 computes its one element twice
         const int v1 = V == 1 ? 0 : v + 1;
-        float2 r, i, a, om, nab = splat(0.f), nib = splat(-kShift);
-        if (params) nab = make_float2(gate_bias(g.a_bias, d + v), gate_bias(g.a_bias, d + v1));
-        if (params) nib = make_float2(gate_bias(g.i_bias, d + v) - kShift, gate_bias(g.i_bias, d + v1) - kShift);
+        float2 r, i, a, om, nab = splat(0.f), nib = splat(0.f);
+        if (g.a_bias && params) nab = make_float2(-kLog2e * __ldg(g.a_bias + d + v), -kLog2e * __ldg(g.a_bias + d + v1));
+        if (g.i_bias && params) nib = make_float2(-kLog2e * __ldg(g.i_bias + d + v), -kLog2e * __ldg(g.i_bias + d + v1));
         const float2 c = !params ? splat(0.f)
                                  : make_float2(decay_rate(__ldg(g.Lam + d + v), g.rate), decay_rate(__ldg(g.Lam + d + v1), g.rate));
         gates2(make_float2(ar[v], ar[v1]), make_float2(ir[v], ir[v1]), nab, nib, r, i);

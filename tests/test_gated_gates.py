@@ -185,3 +185,21 @@ def test_both_gates_at_every_extreme(cuda_device, io, shift):
     half = R.HALF_STEP[dt]
     assert ((R.d64(out) - ref).abs() <= (64 * EPS + half) * ref.abs() + 2.0 ** -61).all()
     assert torch.equal(step, state.to(dt))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 33])
+def test_open_gates_to_a_few_roundings(cuda_device, D):
+    """One token with gates of ordinary size, element by element: h = m i u and a h0 in fp32."""
+    x = R.inputs("gated", 21, "f32", cuda_device, batch=64, length=1, dim=D)
+    x["h0"].zero_()
+    _, last = sb.sscan_gated_fwd(**x, return_last_state=True)
+    _, ref = R.gated(**{k: R.d64(v) for k, v in x.items()})
+    # i: its exponent is rounded to half a step of a number below 8 (2^-22, times ln 2) as is the bias's product (as
+    # much), an exponential of 2 ulp, a sum, a reciprocal of 1 ulp and four products: 22 * 2^-24; m: half of r's as many
+    # and of c's 9, a root of 2 ulp and three products: 23; two products
+    limit = 47 * EPS
+    assert (relative(last, ref) <= limit).all()
+    state = x["h0"].clone()
+    sb.sscan_gated_step(*(x[k][:, 0].contiguous() for k in ("u", "a_raw", "i_raw")), x["Lam"], state, x["a_bias"], x["i_bias"])
+    assert (relative(state, ref) <= limit).all()
